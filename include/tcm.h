@@ -75,7 +75,8 @@ typedef enum tcm_status {
     TCM_ERR_UNSUPPORTED_DTYPE = 5, /* dtype / out_dtype pair not supported */
     TCM_ERR_NO_DEVICE = 6,         /* no HIP device, or it is not gfx950 */
     TCM_ERR_HIP = 7,               /* a HIP runtime call or kernel launch failed */
-    TCM_ERR_INVALID_ARGUMENT = 8   /* an enumeration argument outside its values */
+    TCM_ERR_INVALID_ARGUMENT = 8,  /* an enumeration argument outside its values */
+    TCM_ERR_WORKSPACE = 9          /* the workspace is smaller than the call needs */
 } tcm_status;
 
 typedef enum tcm_dtype {
@@ -304,6 +305,184 @@ typedef struct tcm_plan {
  * other mx values are TCM_ERR_INVALID_ARGUMENT. */
 tcm_status tcm_plan_gemm(int64_t batch, int64_t M, int64_t N, int64_t K, tcm_dtype dtype,
                          tcm_dtype out_dtype, int mx, int num_cus, tcm_plan* plan);
+
+/* ---------------------------------------------------------------------------
+ * The layer around the products: a projection with low-rank adapters, the
+ * norm and rotation of query and key heads, a paged key-value cache and the
+ * attention of one new token over it.
+ *
+ * The conventions above hold (asynchronous on `stream`, validated on the host,
+ * no allocation).  A call that needs scratch memory takes a workspace, a device
+ * buffer of at least the size its *_workspace function gives, 16-byte aligned;
+ * its contents before and after a call mean nothing, and two calls may share
+ * one only if one runs after the other.  Index arrays are int32 in device
+ * memory.  The host cannot look at them, so the kernels check every entry
+ * before they use it; what an entry outside its range means is said at each
+ * call.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * Out[i] = X[i] . W^T + s_a (X[i] . A_a^T) . B_a^T, a = row_adapter[i]: one
+ * shared projection W and, beside it, the low-rank adapter of each row's
+ * request.
+ *   X        M x K, rows ldx >= K elements apart;  W  N x K (dense)
+ *   A        L x R x K;  B  L x N x R: L adapters of rank at most R (dense)
+ *   row_adapter  M adapter numbers in any order; a row whose number is outside
+ *            0 .. L-1 (-1 by custom) has the projection alone
+ *   ranks    NULL, or L ranks: adapter a uses rows 0 .. ranks[a]-1 of A_a and
+ *            the same columns of B_a (clipped to 0 .. R); what lies beyond them
+ *            is not used and may hold anything
+ *   scales   NULL (ones), or L factors s_a in fp32
+ *   Out      M x N of `out_dtype`, rows ldo >= N elements apart
+ * dtype TCM_F16 or TCM_BF16 (X, W, A, B); out_dtype the same or TCM_F32.  All
+ * sums are fp32 and the result is rounded once.  The inner product X[i] . A_a^T
+ * (times s_a) enters the second product as a sum of two 16-bit values, which
+ * hold its upper 16 bits (TCM_F16: 22; there its magnitude must stay below
+ * 65520, past which the row's output is infinite or NaN).  A row's output
+ * depends on its own adapter only: values that are not finite in one adapter
+ * do not reach the rows of another.
+ * R a multiple of 8, at most 128; K a multiple of 8 (TCM_ERR_MISALIGNED
+ * otherwise); ldx a multiple of 8 and at most 2^21; X, W, A, B and Out 16-byte
+ * aligned.  L == 0 or R == 0 gives the projection alone.
+ */
+tcm_status tcm_lora_gemm_tn(const void* X, int64_t ldx, const void* W, const void* A,
+                            const void* B, const int32_t* row_adapter, const int32_t* ranks,
+                            const float* scales, void* Out, int64_t ldo, int64_t M, int64_t N,
+                            int64_t K, int64_t L, int64_t R, tcm_dtype dtype, tcm_dtype out_dtype,
+                            void* workspace, int64_t workspace_bytes, void* stream);
+tcm_status tcm_lora_workspace(int64_t M, int64_t K, int64_t R, int64_t* bytes);
+
+/* A view of T tokens x H heads x D elements, the D elements of a head
+ * contiguous: element (t, h, d) at ptr[t * token_stride + h * head_stride + d].
+ * 16-byte aligned, strides multiples of 8 elements (TCM_ERR_MISALIGNED); so a
+ * slice of the heads of a fused projection is a view.  Views that a call writes
+ * must not overlap themselves or each other. */
+typedef struct tcm_heads {
+    void* ptr;
+    int64_t token_stride, head_stride;
+} tcm_heads;
+
+/* A paged cache of keys and values: `pages` pages of `page_size` tokens of every
+ * key-value head.  Key (p, s, h, d) lies at k[p * k_page_stride + s *
+ * k_token_stride + h * k_head_stride + d], values the same way with their own
+ * strides (so tokens-first and heads-first pages are both views).  dtype is
+ * the type of the calls that use it, or TCM_E4M3, which stands for
+ * k_scale * element and v_scale * element (the scales are not looked at
+ * otherwise).  16-byte aligned, strides whole 16-byte pieces
+ * (TCM_ERR_MISALIGNED); page_size at most 2^20. */
+typedef struct tcm_cache {
+    void* k;
+    void* v;
+    int64_t pages, page_size;
+    int64_t k_page_stride, k_token_stride, k_head_stride;
+    int64_t v_page_stride, v_token_stride, v_head_stride;
+    int32_t dtype; /* a tcm_dtype */
+    float k_scale, v_scale;
+} tcm_cache;
+
+/* Which elements of the rotated part of a head form a pair. */
+typedef enum tcm_rope_layout {
+    TCM_ROPE_HALF = 0,        /* j and j + rot_dim / 2 */
+    TCM_ROPE_INTERLEAVED = 1  /* 2 j and 2 j + 1 */
+} tcm_rope_layout;
+
+/*
+ * The norm and rotation of one head x (D elements):
+ *   n = x w / sqrt(mean(x^2) + eps)     (norm != 0; w ones where its pointer is NULL)
+ *   n = x                               (norm == 0)
+ * and the pairs (n1, n2) of the first rot_dim elements turned by the angle
+ * t = position * inv_freq[j]:
+ *   y1 = factor (n1 cos t - n2 sin t),  y2 = factor (n2 cos t + n1 sin t);
+ * the other D - rot_dim elements are n.  The angle is computed and reduced in 64
+ * bits, so it is exact to 1e-7 for every int32 position; tables are not needed,
+ * and a scaling for long contexts is a choice of inv_freq and factor.
+ *   head_dim  D, a multiple of 8, at most 256 (TCM_ERR_UNSUPPORTED_SHAPE)
+ *   rot_dim   even, 0 .. D (TCM_ERR_INVALID_SHAPE)
+ *   positions T int32;  inv_freq  rot_dim / 2 doubles (both NULL if rot_dim == 0)
+ *   q_weight, k_weight  D elements of weight_dtype: TCM_F32 or the call's dtype
+ */
+typedef struct tcm_rope {
+    int64_t head_dim, rot_dim;
+    const int32_t* positions;
+    const double* inv_freq;
+    float factor;
+    int32_t layout; /* a tcm_rope_layout */
+    int32_t norm;
+    float eps;
+    const void* q_weight;
+    const void* k_weight;
+    int32_t weight_dtype; /* a tcm_dtype */
+} tcm_rope;
+
+/*
+ * q_out = rope(norm(q)) for Hq query heads and k_out = rope(norm(k)) for Hk key
+ * heads of T tokens, in one pass.  dtype TCM_F16 or TCM_BF16; computed in fp32
+ * and rounded once.  Hq or Hk may be 0 (their views are then not looked at).
+ * q_out may be q and k_out may be k (the same pointer and strides).
+ */
+tcm_status tcm_qk_norm_rope(const tcm_heads* q, const tcm_heads* k, const tcm_heads* q_out,
+                            const tcm_heads* k_out, int64_t T, int64_t Hq, int64_t Hk,
+                            const tcm_rope* rope, tcm_dtype dtype, void* stream);
+
+/*
+ * The same with the keys, and the values v as they are, written into a cache:
+ * token t goes to slot slots[t] = page * page_size + place in the page.  A slot
+ * outside 0 .. pages * page_size - 1 (-1 by custom) writes nothing to the cache;
+ * its query is computed all the same.  No two tokens may have the same slot.
+ * TCM_E4M3 caches take x / scale, clamped to +-448 and rounded to nearest
+ * even (NaN stays NaN).
+ */
+tcm_status tcm_qk_norm_rope_cache(const tcm_heads* q, const tcm_heads* k, const tcm_heads* v,
+                                  const tcm_heads* q_out, const tcm_cache* cache,
+                                  const int32_t* slots, int64_t T, int64_t Hq, int64_t Hk,
+                                  const tcm_rope* rope, tcm_dtype dtype, void* stream);
+
+/*
+ * Gradients of tcm_qk_norm_rope: from dq_out, dk_out (of its outputs) and its
+ * inputs q, k those of the inputs, dq, dk (rounded once to dtype), and of the
+ * weights, dq_weight, dk_weight (D fp32 sums over tokens and heads, overwritten;
+ * NULL: not computed).  With g = w rot^T(dy) and h = x / sqrt(mean(x^2) + eps):
+ *   dx = (g - h mean(g h)) / sqrt(mean(x^2) + eps),  dw = sum rot^T(dy) h.
+ * Sums run in a fixed order: the same call gives the same bits.  dq may be
+ * dq_out and dk dk_out.  T == 0 gives zero weight gradients.
+ */
+tcm_status tcm_qk_norm_rope_bwd(const tcm_heads* dq_out, const tcm_heads* dk_out,
+                                const tcm_heads* q, const tcm_heads* k, const tcm_heads* dq,
+                                const tcm_heads* dk, float* dq_weight, float* dk_weight, int64_t T,
+                                int64_t Hq, int64_t Hk, const tcm_rope* rope, tcm_dtype dtype,
+                                void* workspace, int64_t workspace_bytes, void* stream);
+tcm_status tcm_qk_norm_rope_bwd_workspace(int64_t head_dim, int64_t* bytes);
+
+/*
+ * Attention of one new token per sequence over a paged cache: for sequence b
+ * and query head h (key-value head h / (Hq / Hk)),
+ *   out = sum_j p_j v_j,  p = softmax_j(scale * q . k_j),
+ * j over the keys max(0, n - window) .. n - 1 of the sequence (window == 0: all),
+ * n = lengths[b].  Key j lies in page block_table[b * table_stride + j / page_size]
+ * at place j % page_size.
+ *   q, out   views of B tokens x Hq heads x D; out may be q
+ *   block_table  B rows of table_stride entries; an entry outside 0 .. pages-1
+ *            is a hole, whose keys are not attended
+ *   lengths  B int32, clipped to 0 .. min(max_len, table_stride * page_size)
+ *   lse      NULL, or B x Hq fp32 (dense): log sum_j exp(scale * q . k_j)
+ *   max_len  an upper bound of the lengths, which the split over the length
+ *            goes by (a graph captured with it serves every length up to it)
+ * A sequence without keys gives out = 0 and lse = -infinity.  Cache memory
+ * that holds no attended key is not used and may hold anything.
+ * dtype (q, out) TCM_F16 or TCM_BF16, the cache's dtype the same or TCM_E4M3.  Scores,
+ * softmax and sums in fp32; the probabilities enter the second product rounded
+ * to dtype.  D a multiple of 8 (16 for TCM_E4M3 caches), at most 256; Hq a multiple of
+ * Hk; B and Hq at most 65535.
+ */
+tcm_status tcm_paged_attention(const tcm_heads* q, const tcm_cache* cache,
+                               const int32_t* block_table, int64_t table_stride,
+                               const int32_t* lengths, int64_t max_len, const tcm_heads* out,
+                               float* lse, int64_t B, int64_t Hq, int64_t Hk, int64_t D,
+                               float scale, int64_t window, tcm_dtype dtype, void* workspace,
+                               int64_t workspace_bytes, void* stream);
+/* (enough also for smaller max_len and for every window) */
+tcm_status tcm_paged_attention_workspace(int64_t B, int64_t Hq, int64_t Hk, int64_t D,
+                                         int64_t max_len, int64_t* bytes);
 
 /* Static, human-readable name of a status code, the counterpart of the error
  * string lookup of "API Card: Blackwell Pipeline (tcgen05)", Host side.

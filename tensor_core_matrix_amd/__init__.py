@@ -21,6 +21,15 @@ kernels; there is no fallback.  If the library is missing, every call raises.
                                                        and b: K x N strided views
     gemm_mx(a, b, scale_a, scale_b, out=None, out_dtype=None)
                                                        MXFP8, a: M x K and b: K x N strided views
+
+The layer around the products (``layer.py``, the same library):
+
+    lora_gemm_tn(x, w, lora_a, lora_b, row_adapter, ...)   projection with many requests' adapters
+    qk_norm_rope(q, k, positions, inv_freq, ...)           norm and rotation of heads
+    qk_norm_rope_cache(q, k, v, ...)                       the same, into a paged cache
+    qk_norm_rope_bwd(dq_out, dk_out, q, k, ...)            its gradients
+    paged_attention(q, k_cache, v_cache, ...)              one new token per sequence
+    rope_frequencies(rot_dim, base, scaling, ...)          inv_freq and factor
 """
 from __future__ import annotations
 
@@ -31,7 +40,9 @@ import threading
 __all__ = ["gemm", "gemm_tn", "gemm_tn_ex", "batched_gemm_tn", "gemm_mx_fp8", "gemm_mx_fp4",
            "gemm_mx_fp6", "gemm_nvfp4", "gemm_mx", "order_ld", "plan", "lib", "TcmError",
            "LIB_PATH", "F16", "BF16", "F32", "E4M3", "E8M0", "E2M1", "E2M3", "E3M2", "ROW_MAJOR",
-           "COL_MAJOR", "OPS"]
+           "COL_MAJOR", "OPS", "lora_gemm_tn", "lora_workspace", "qk_norm_rope", "qk_norm_rope_cache",
+           "qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace", "paged_attention",
+           "paged_attention_workspace", "rope_frequencies"]
 
 # TCM_LIBRARY names another build of the same library (the host-sanitizer
 # build of `python -m tensor_core_matrix_amd.build --sanitize`); by default
@@ -64,16 +75,42 @@ class Plan(ctypes.Structure):
         return {name: getattr(self, name) for name, _ in self._fields_}
 
 
+class Heads(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int64), ("k_page_stride", ctypes.c_int64),
+                ("k_token_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+                ("v_page_stride", ctypes.c_int64), ("v_token_stride", ctypes.c_int64),
+                ("v_head_stride", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int64), ("rot_dim", ctypes.c_int64),
+                ("positions", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p),
+                ("factor", ctypes.c_float), ("layout", ctypes.c_int32), ("norm", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p), ("weight_dtype", ctypes.c_int32)]
+
+
 _lock = threading.Lock()
 _lib = None
 EXPORTS = ("tcm_gemm", "tcm_gemm_tn", "tcm_gemm_tn_ex", "tcm_batched_gemm_tn", "tcm_gemm_mx_fp8",
            "tcm_gemm_mx_fp4", "tcm_gemm_mx_fp6", "tcm_gemm_mx", "tcm_gemm_nvfp4", "tcm_plan_gemm",
-           "tcm_status_string")
+           "tcm_status_string", "tcm_lora_gemm_tn", "tcm_lora_workspace", "tcm_qk_norm_rope",
+           "tcm_qk_norm_rope_cache", "tcm_qk_norm_rope_bwd", "tcm_qk_norm_rope_bwd_workspace",
+           "tcm_paged_attention", "tcm_paged_attention_workspace")
 
 
 def lib() -> ctypes.CDLL:
     """The loaded libtcm (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -94,11 +131,27 @@ def lib() -> ctypes.CDLL:
             L.tcm_gemm_mx.argtypes = [vp, ci, i64, vp, ci, i64, vp, vp, vp, i64, i64, i64, i64, ci,
                                       ci, vp]
             L.tcm_plan_gemm.argtypes = [i64, i64, i64, i64, ci, ci, ci, ci, ctypes.POINTER(Plan)]
+            hd, ca, ro = (ctypes.POINTER(t) for t in (Heads, Cache, Rope))
+            pi64 = ctypes.POINTER(i64)
+            L.tcm_lora_gemm_tn.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64,
+                                           i64, i64, ci, ci, vp, i64, vp]
+            L.tcm_lora_workspace.argtypes = [i64, i64, i64, pi64]
+            L.tcm_qk_norm_rope.argtypes = [hd, hd, hd, hd, i64, i64, i64, ro, ci, vp]
+            L.tcm_qk_norm_rope_cache.argtypes = [hd, hd, hd, hd, ca, vp, i64, i64, i64, ro, ci, vp]
+            L.tcm_qk_norm_rope_bwd.argtypes = [hd, hd, hd, hd, hd, hd, vp, vp, i64, i64, i64, ro, ci,
+                                               vp, i64, vp]
+            L.tcm_qk_norm_rope_bwd_workspace.argtypes = [i64, pi64]
+            L.tcm_paged_attention.argtypes = [hd, ca, vp, i64, vp, i64, hd, vp, i64, i64, i64, i64,
+                                              cf, i64, ci, vp, i64, vp]
+            L.tcm_paged_attention_workspace.argtypes = [i64, i64, i64, i64, i64, pi64]
             L.tcm_status_string.argtypes = [ci]
             L.tcm_status_string.restype = ctypes.c_char_p
             for f in ("tcm_gemm", "tcm_gemm_tn", "tcm_gemm_tn_ex", "tcm_batched_gemm_tn", "tcm_gemm_mx_fp8",
                       "tcm_gemm_mx_fp4", "tcm_gemm_mx_fp6", "tcm_gemm_mx", "tcm_gemm_nvfp4",
-                      "tcm_plan_gemm"):
+                      "tcm_plan_gemm", "tcm_lora_gemm_tn", "tcm_lora_workspace", "tcm_qk_norm_rope",
+                      "tcm_qk_norm_rope_cache", "tcm_qk_norm_rope_bwd",
+                      "tcm_qk_norm_rope_bwd_workspace", "tcm_paged_attention",
+                      "tcm_paged_attention_workspace"):
                 getattr(L, f).restype = ci
             _lib = L
     return _lib
@@ -408,3 +461,8 @@ def plan(M, N, K, dtype=BF16, out_dtype=BF16, batch=1, mx=False, num_cus=256) ->
     _check(lib().tcm_plan_gemm(batch, M, N, K, dtype, out_dtype, int(mx), num_cus,
                                ctypes.byref(p)))
     return p.as_dict()
+
+
+from .layer import (lora_gemm_tn, lora_workspace, paged_attention, paged_attention_workspace,  # noqa: E402
+                    qk_norm_rope, qk_norm_rope_bwd, qk_norm_rope_bwd_workspace, qk_norm_rope_cache,
+                    rope_frequencies)

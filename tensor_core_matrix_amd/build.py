@@ -7,7 +7,7 @@ Each source is compiled by hipcc in parallel, then linked into
 assembly of every kernel source to DIR for inspection.
 
 ``--sanitize`` builds ``_build/libtcm_san.so`` instead: the host code (the
-C ABI, validation, planning and dispatch in tcm_api.cpp) compiled by g++
+C ABI, validation, planning and dispatch in the .cpp sources) compiled by g++
 with AddressSanitizer and UndefinedBehaviorSanitizer, linked with the
 ordinary device objects.  It is for CPU runs of the host-side tests, e.g.
 
@@ -16,7 +16,7 @@ ordinary device objects.  It is for CPU runs of the host-side tests, e.g.
     LD_PRELOAD=$(gcc -print-file-name=libasan.so):$(gcc -print-file-name=libubsan.so) \
     ASAN_OPTIONS=detect_leaks=0 UBSAN_OPTIONS=halt_on_error=1:print_stacktrace=1 \
     TCM_LIBRARY=_build/libtcm_san.so ORACLE_LIBRARY=oracle/liboracle_san.so \
-    python -m pytest tests/test_abi.py tests/test_oracle.py -m "not gpu"
+    python -m pytest tests/test_abi.py tests/test_layer_abi.py tests/test_oracle.py -m "not gpu"
 """
 from __future__ import annotations
 
@@ -38,7 +38,8 @@ SANITIZE = ["-fsanitize=address,undefined", "-fno-omit-frame-pointer", "-g"]
 ARCH = "gfx950"
 SOURCES = ["tcm_api.cpp", "gemm_tn.hip", "gemm_mx.hip", "gemm_mx6.hip", "gemm_nv4.hip", "gemm_epi.hip",
            "gemm_mn_a.hip", "gemm_mn_b.hip", "gemm_mn_ab.hip", "gemm_mx_ld.hip", "gemm_mx_mn_a.hip",
-           "gemm_mx_mn_b.hip", "gemm_mx_mn_ab.hip"]
+           "gemm_mx_mn_b.hip", "gemm_mx_mn_ab.hip", "layer_api.cpp", "lora.hip", "rope.hip",
+           "paged_attn.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-I", os.path.join(ROOT, "include")]
@@ -85,7 +86,7 @@ def build(asm_dir: str | None = None, verbose: bool = True) -> str:
 
 
 def build_sanitized(verbose: bool = True) -> str:
-    """_build/libtcm_san.so: tcm_api.cpp with the sanitizers (g++), linked by
+    """_build/libtcm_san.so: the .cpp sources with the sanitizers (g++), linked by
     g++ with the device objects of an ordinary build (built here if absent)."""
     os.makedirs(BUILD, exist_ok=True)
     dev = [s for s in SOURCES if s.endswith(".hip")]
@@ -93,8 +94,8 @@ def build_sanitized(verbose: bool = True) -> str:
     missing = [s for s, o in zip(dev, objs) if not os.path.exists(o)]
     with cf.ThreadPoolExecutor(max_workers=max(1, len(missing))) as ex:
         list(ex.map(lambda s: _compile(s, None), missing))
-    host = _compile("tcm_api.cpp", None, sanitize=True)
-    subprocess.run(["g++", "-shared", *SANITIZE, host, *objs, "-o", SAN_LIB,
+    host = [_compile(s, None, sanitize=True) for s in SOURCES if not s.endswith(".hip")]
+    subprocess.run(["g++", "-shared", *SANITIZE, *host, *objs, "-o", SAN_LIB,
                     "-L/opt/rocm/lib", "-lamdhip64", "-Wl,-rpath,/opt/rocm/lib"], check=True)
     if verbose:
         print(f"built {SAN_LIB}")

@@ -1,0 +1,429 @@
+// C ABI of the layer operators (adapters, norm and rotation of heads, paged
+// attention): argument validation and dispatch, in the order of tcm_api.cpp:
+// dtypes and enumerations, sizes, pointers, supported range, alignment, workspace.
+#include <limits.h>
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+
+#include <hip/hip_runtime.h>
+
+#include "../../include/tcm.h"
+#include "layer_internal.h"
+#include "tcm_host.h"
+
+namespace {
+
+using namespace tcm;
+
+constexpr int64_t kMaxK = int64_t(1) << 20;
+constexpr int64_t kMaxLd = int64_t(1) << 21;   // 256 rows of it stay within 32 bits
+constexpr int64_t kMaxRows = int64_t(1) << 30;
+constexpr int64_t kMaxHeads = 65535;
+// a stride (elements) and its product with a count stay far from 64 bits
+constexpr int64_t kMaxStride = int64_t(1) << 40;
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+bool half_type(tcm_dtype d) { return d == TCM_F16 || d == TCM_BF16; }
+
+tcm_status launched(hipError_t e) { return e == hipSuccess ? TCM_OK : TCM_ERR_HIP; }
+
+// ---- views ----------------------------------------------------------------------
+
+tcm_status check_heads(const tcm_heads* v) {
+    if (!v || !v->ptr) return TCM_ERR_NULL_POINTER;
+    if (v->token_stride < 0 || v->head_stride < 0 || v->token_stride > kMaxStride ||
+        v->head_stride > kMaxStride)
+        return TCM_ERR_INVALID_SHAPE;
+    if (!aligned16(v->ptr) || v->token_stride % 8 != 0 || v->head_stride % 8 != 0)
+        return TCM_ERR_MISALIGNED;
+    return TCM_OK;
+}
+
+// A view that is written: its tokens and heads lie apart.
+tcm_status check_written(const tcm_heads* v, int64_t T, int64_t H, int64_t D) {
+    tcm_status s = check_heads(v);
+    if (s != TCM_OK) return s;
+    const int64_t ts = v->token_stride, hs = v->head_stride;
+    if (T > 1 && H > 1) {
+        // one of the two is the outer one and steps over the whole of the other
+        const bool tokens_outer = hs >= D && ts >= (H - 1) * hs + D;
+        const bool heads_outer = ts >= D && hs >= (T - 1) * ts + D;
+        if (!tokens_outer && !heads_outer) return TCM_ERR_INVALID_SHAPE;
+    } else if ((T > 1 && ts < D) || (H > 1 && hs < D)) {
+        return TCM_ERR_INVALID_SHAPE;
+    }
+    return TCM_OK;
+}
+
+HeadView view(const tcm_heads* v) { return {v->ptr, v->token_stride, v->head_stride}; }
+
+tcm_status check_cache(const tcm_cache* c, tcm_dtype dtype, int64_t Hk, int64_t D, bool written) {
+    if (!c) return TCM_ERR_NULL_POINTER;
+    if (c->dtype != dtype && c->dtype != TCM_E4M3) return TCM_ERR_UNSUPPORTED_DTYPE;
+    if (c->pages < 0 || c->page_size < 1) return TCM_ERR_INVALID_SHAPE;
+    const int64_t st[6] = {c->k_page_stride, c->k_token_stride, c->k_head_stride,
+                           c->v_page_stride, c->v_token_stride, c->v_head_stride};
+    for (int64_t s : st)
+        if (s < 0 || s > kMaxStride) return TCM_ERR_INVALID_SHAPE;
+    if (written) {
+        // every (page, place, head) its own D elements at least
+        for (int i = 0; i < 6; i += 3) {
+            if ((c->pages > 1 && st[i] < D) || (c->page_size > 1 && st[i + 1] < D) ||
+                (Hk > 1 && st[i + 2] < D))
+                return TCM_ERR_INVALID_SHAPE;
+        }
+    }
+    if (c->pages > 0 && (!c->k || !c->v)) return TCM_ERR_NULL_POINTER;
+    if (c->pages > INT32_MAX || c->page_size > (int64_t(1) << 20)) return TCM_ERR_UNSUPPORTED_SHAPE;
+    const int64_t piece = c->dtype == TCM_E4M3 ? 16 : 8;
+    for (int64_t s : st)
+        if (s % piece != 0) return TCM_ERR_MISALIGNED;
+    if (!aligned16(c->k) || !aligned16(c->v)) return TCM_ERR_MISALIGNED;
+    return TCM_OK;
+}
+
+// ---- norm and rotation -------------------------------------------------------------
+
+tcm_status check_rope(const tcm_rope* r, tcm_dtype dtype, int64_t T, int64_t Hq, int64_t Hk) {
+    if (!half_type(dtype)) return TCM_ERR_UNSUPPORTED_DTYPE;
+    if (!r) return TCM_ERR_NULL_POINTER;
+    if (r->layout != TCM_ROPE_HALF && r->layout != TCM_ROPE_INTERLEAVED) return TCM_ERR_INVALID_ARGUMENT;
+    const bool weighted = r->norm && (r->q_weight || r->k_weight);
+    if (weighted && r->weight_dtype != dtype && r->weight_dtype != TCM_F32) return TCM_ERR_UNSUPPORTED_DTYPE;
+    if (T < 0 || Hq < 0 || Hk < 0 || r->head_dim < 1 || r->rot_dim < 0 || r->rot_dim > r->head_dim ||
+        r->rot_dim % 2 != 0)
+        return TCM_ERR_INVALID_SHAPE;
+    if (T > kMaxRows || Hq > kMaxHeads || Hk > kMaxHeads || r->head_dim > kMaxHeadDim ||
+        r->head_dim % 8 != 0)
+        return TCM_ERR_UNSUPPORTED_SHAPE;
+    if (T > 0 && Hq + Hk > 0 && r->rot_dim > 0 && (!r->positions || !r->inv_freq))
+        return TCM_ERR_NULL_POINTER;
+    return TCM_OK;
+}
+
+void fill_rope(RopeArgs* a, const tcm_rope* r, int64_t T, int64_t Hq, int64_t Hk) {
+    memset(a, 0, sizeof(*a));
+    a->pos = r->positions;
+    a->inv_freq = r->inv_freq;
+    a->wq = r->norm ? r->q_weight : nullptr;
+    a->wk = r->norm ? r->k_weight : nullptr;
+    a->eps = r->eps;
+    a->factor = r->factor;
+    a->T = (int32_t)T;
+    a->Hq = (int32_t)Hq;
+    a->Hk = (int32_t)Hk;
+    a->D = (int32_t)r->head_dim;
+    a->rot = (int32_t)r->rot_dim;
+    a->norm = r->norm != 0;
+    a->w_f32 = r->weight_dtype == TCM_F32;
+}
+
+int64_t bwd_workspace(int64_t D) { return int64_t(kRopeBwdGrid) * 2 * D * 4; }
+
+// ---- paged attention ----------------------------------------------------------------
+
+// The split over the length: chunks (of whole 128-key rounds of a workgroup)
+// such that about 1024 workgroups share the work, four for every compute unit,
+// but none with fewer than 256 keys.
+constexpr int64_t kMinChunk = 256;
+struct Split {
+    int64_t chunk, n;
+};
+int64_t most_splits(int64_t B, int64_t Hq, int64_t Hk) {
+    const int64_t units = B * Hk * cdiv(Hq / Hk, 16);
+    const int64_t n = cdiv(1024, units > 0 ? units : 1);
+    return n < kAttnMaxSplits ? n : kAttnMaxSplits;
+}
+Split split_of(int64_t B, int64_t Hq, int64_t Hk, int64_t span) {
+    int64_t chunk = cdiv(cdiv(span, most_splits(B, Hq, Hk)), 128) * 128;
+    if (chunk < kMinChunk) chunk = kMinChunk;
+    const int64_t n = cdiv(span, chunk);
+    return {chunk, n > 0 ? n : 1};
+}
+int64_t attn_workspace(int64_t B, int64_t Hq, int64_t D, int64_t n) {
+    return n > 1 ? B * Hq * n * (D + 2) * 4 : 0;
+}
+
+tcm_status check_attn_sizes(int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t max_len) {
+    if (B < 0 || Hq < 0 || Hk < 0 || D < 1 || max_len < 0) return TCM_ERR_INVALID_SHAPE;
+    if ((Hq > 0 && Hk == 0) || (Hk > 0 && Hq % Hk != 0)) return TCM_ERR_INVALID_SHAPE;
+    if (B > kMaxHeads || Hq > kMaxHeads || D > kMaxHeadDim || D % 8 != 0 || max_len > kMaxRows)
+        return TCM_ERR_UNSUPPORTED_SHAPE;
+    return TCM_OK;
+}
+
+// ---- adapters ------------------------------------------------------------------------
+
+// Parts of K in the adapters' first product: with few rows there are few (block,
+// adapter) pairs, and K is what is left to spread over the compute units; a
+// part is at least 512 values, two steps of each of a workgroup's eight waves.
+int64_t lora_parts(int64_t M, int64_t K, int64_t* kpart) {
+    int64_t n = M > 0 ? 256 / M : 1;
+    if (n > 8) n = 8;
+    if (n > K / 512) n = K / 512;
+    if (n < 1) n = 1;
+    *kpart = cdiv(cdiv(K, n), 256) * 256;
+    if (*kpart < 256) *kpart = 256;
+    n = cdiv(K, *kpart);
+    return n > 0 ? n : 1;
+}
+
+tcm_status check_lora_sizes(int64_t M, int64_t K, int64_t R) {
+    if (M < 0 || K < 0 || R < 0) return TCM_ERR_INVALID_SHAPE;
+    if (M > kMaxRows || K > kMaxK || R > kLoraMaxRank) return TCM_ERR_UNSUPPORTED_SHAPE;
+    return TCM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+tcm_status tcm_lora_workspace(int64_t M, int64_t K, int64_t R, int64_t* bytes) {
+    if (!bytes) return TCM_ERR_NULL_POINTER;
+    tcm_status s = check_lora_sizes(M, K, R);
+    if (s != TCM_OK) return s;
+    int64_t kpart;
+    *bytes = lora_parts(M, K, &kpart) * M * R * 4;
+    return TCM_OK;
+}
+
+tcm_status tcm_lora_gemm_tn(const void* X, int64_t ldx, const void* W, const void* A,
+                            const void* B, const int32_t* row_adapter, const int32_t* ranks,
+                            const float* scales, void* Out, int64_t ldo, int64_t M, int64_t N,
+                            int64_t K, int64_t L, int64_t R, tcm_dtype dtype, tcm_dtype out_dtype,
+                            void* workspace, int64_t workspace_bytes, void* stream) {
+    if (!half_type(dtype) || !(out_dtype == dtype || out_dtype == TCM_F32))
+        return TCM_ERR_UNSUPPORTED_DTYPE;
+    if (N < 0 || L < 0 || ldx < (K > 1 ? K : 1) || ldo < (N > 1 ? N : 1)) return TCM_ERR_INVALID_SHAPE;
+    tcm_status s = check_lora_sizes(M, K, R);
+    if (s != TCM_OK) return s;
+    if (N > kMaxRows || L > kMaxRows || ldx > kMaxLd || ldo > INT32_MAX) return TCM_ERR_UNSUPPORTED_SHAPE;
+    if (cdiv(M, 64) * cdiv(N, 64) > INT32_MAX) return TCM_ERR_UNSUPPORTED_SHAPE;
+    if (M == 0 || N == 0) return TCM_OK;
+    const bool adapters = L > 0 && R > 0 && K > 0;
+    if (!Out || (K > 0 && (!X || !W)) || (adapters && (!A || !B || !row_adapter || !workspace)))
+        return TCM_ERR_NULL_POINTER;
+    if (!aligned16(X) || !aligned16(W) || !aligned16(Out) || K % 8 != 0 || ldx % 8 != 0 ||
+        (adapters && (!aligned16(A) || !aligned16(B) || !aligned16(workspace) || R % 8 != 0)))
+        return TCM_ERR_MISALIGNED;
+    LoraArgs a;
+    memset(&a, 0, sizeof(a));
+    int64_t kpart;
+    const int64_t parts = lora_parts(M, K, &kpart);
+    if (adapters && workspace_bytes < parts * M * R * 4) return TCM_ERR_WORKSPACE;
+    DeviceInfo dev;
+    if ((s = device_info(&dev)) != TCM_OK) return s;
+    a.X = X;
+    a.W = W;
+    a.A = A;
+    a.B = B;
+    a.rows = row_adapter;
+    a.ranks = ranks;
+    a.scales = scales;
+    a.out = Out;
+    a.t = (float*)workspace;
+    a.M = (int32_t)M;
+    a.N = (int32_t)N;
+    a.K = (int32_t)K;
+    a.L = adapters ? (int32_t)L : 0;
+    a.R = (int32_t)R;
+    a.ldx = (int32_t)ldx;
+    a.ldo = (int32_t)ldo;
+    a.ksplit = (int32_t)parts;
+    a.kpart = (int32_t)kpart;
+    return launched(launch_lora(a, (int32_t)dtype, (int32_t)out_dtype, dev.cus, (hipStream_t)stream));
+}
+
+tcm_status tcm_qk_norm_rope(const tcm_heads* q, const tcm_heads* k, const tcm_heads* q_out,
+                            const tcm_heads* k_out, int64_t T, int64_t Hq, int64_t Hk,
+                            const tcm_rope* rope, tcm_dtype dtype, void* stream) {
+    tcm_status s = check_rope(rope, dtype, T, Hq, Hk);
+    if (s != TCM_OK || T == 0 || Hq + Hk == 0) return s;
+    const int64_t D = rope->head_dim;
+    if (Hq > 0 && ((s = check_heads(q)) != TCM_OK || (s = check_written(q_out, T, Hq, D)) != TCM_OK)) return s;
+    if (Hk > 0 && ((s = check_heads(k)) != TCM_OK || (s = check_written(k_out, T, Hk, D)) != TCM_OK)) return s;
+    DeviceInfo dev;
+    if ((s = device_info(&dev)) != TCM_OK) return s;
+    RopeArgs a;
+    fill_rope(&a, rope, T, Hq, Hk);
+    if (Hq > 0) a.q = view(q), a.qo = view(q_out);
+    if (Hk > 0) a.k = view(k), a.ko = view(k_out);
+    return launched(launch_norm_rope(a, (int32_t)dtype, (int32_t)rope->layout, (hipStream_t)stream));
+}
+
+tcm_status tcm_qk_norm_rope_cache(const tcm_heads* q, const tcm_heads* k, const tcm_heads* v,
+                                  const tcm_heads* q_out, const tcm_cache* cache,
+                                  const int32_t* slots, int64_t T, int64_t Hq, int64_t Hk,
+                                  const tcm_rope* rope, tcm_dtype dtype, void* stream) {
+    tcm_status s = check_rope(rope, dtype, T, Hq, Hk);
+    if (s != TCM_OK) return s;
+    const int64_t D = rope->head_dim;
+    if ((s = check_cache(cache, dtype, Hk, D, true)) != TCM_OK) return s;
+    if (T == 0 || Hq + Hk == 0) return TCM_OK;
+    if (!slots) return TCM_ERR_NULL_POINTER;
+    if (Hq > 0 && ((s = check_heads(q)) != TCM_OK || (s = check_written(q_out, T, Hq, D)) != TCM_OK)) return s;
+    if (Hk > 0 && ((s = check_heads(k)) != TCM_OK || (s = check_heads(v)) != TCM_OK)) return s;
+    DeviceInfo dev;
+    if ((s = device_info(&dev)) != TCM_OK) return s;
+    RopeArgs a;
+    fill_rope(&a, rope, T, Hq, Hk);
+    if (Hq > 0) a.q = view(q), a.qo = view(q_out);
+    if (Hk > 0) a.k = view(k), a.v = view(v);
+    a.Hv = (int32_t)Hk;
+    a.slots = slots;
+    a.num_slots = cache->pages * cache->page_size;
+    a.page_size = (int32_t)cache->page_size;
+    a.cache_e4m3 = cache->dtype == TCM_E4M3;
+    const int64_t es = a.cache_e4m3 ? 1 : 2;
+    a.kc = cache->k;
+    a.vc = cache->v;
+    a.k_page = cache->k_page_stride * es;
+    a.k_tok = cache->k_token_stride * es;
+    a.k_head = cache->k_head_stride * es;
+    a.v_page = cache->v_page_stride * es;
+    a.v_tok = cache->v_token_stride * es;
+    a.v_head = cache->v_head_stride * es;
+    a.k_inv = 1.0f / cache->k_scale;
+    a.v_inv = 1.0f / cache->v_scale;
+    return launched(launch_norm_rope(a, (int32_t)dtype, (int32_t)rope->layout, (hipStream_t)stream));
+}
+
+tcm_status tcm_qk_norm_rope_bwd_workspace(int64_t head_dim, int64_t* bytes) {
+    if (!bytes) return TCM_ERR_NULL_POINTER;
+    if (head_dim < 1) return TCM_ERR_INVALID_SHAPE;
+    if (head_dim > kMaxHeadDim || head_dim % 8 != 0) return TCM_ERR_UNSUPPORTED_SHAPE;
+    *bytes = bwd_workspace(head_dim);
+    return TCM_OK;
+}
+
+tcm_status tcm_qk_norm_rope_bwd(const tcm_heads* dq_out, const tcm_heads* dk_out,
+                                const tcm_heads* q, const tcm_heads* k, const tcm_heads* dq,
+                                const tcm_heads* dk, float* dq_weight, float* dk_weight, int64_t T,
+                                int64_t Hq, int64_t Hk, const tcm_rope* rope, tcm_dtype dtype,
+                                void* workspace, int64_t workspace_bytes, void* stream) {
+    tcm_status s = check_rope(rope, dtype, T, Hq, Hk);
+    if (s != TCM_OK) return s;
+    const int64_t D = rope->head_dim;
+    const bool any = T > 0 && Hq + Hk > 0, dw = dq_weight || dk_weight;
+    // (without the norm there are no weights)
+    if (dw && !rope->norm) return TCM_ERR_INVALID_ARGUMENT;
+    if (!any && !dw) return TCM_OK;
+    for (int i = 0; any && i < 2; ++i) {
+        const int64_t H = i ? Hk : Hq;
+        if (H == 0) continue;
+        if ((s = check_heads(i ? dk_out : dq_out)) != TCM_OK) return s;
+        if (rope->norm && (s = check_heads(i ? k : q)) != TCM_OK) return s;
+        if ((s = check_written(i ? dk : dq, T, H, D)) != TCM_OK) return s;
+    }
+    if (dw) {
+        if (!workspace) return TCM_ERR_NULL_POINTER;
+        if (!aligned16(workspace)) return TCM_ERR_MISALIGNED;
+        if (workspace_bytes < bwd_workspace(D)) return TCM_ERR_WORKSPACE;
+    }
+    DeviceInfo dev;
+    if ((s = device_info(&dev)) != TCM_OK) return s;
+    RopeArgs a;
+    fill_rope(&a, rope, any ? T : 0, Hq, Hk);
+    if (any && Hq > 0) {
+        a.dqo = view(dq_out), a.qo = view(dq);
+        if (rope->norm) a.q = view(q);
+    }
+    if (any && Hk > 0) {
+        a.dko = view(dk_out), a.ko = view(dk);
+        if (rope->norm) a.k = view(k);
+    }
+    a.partial = dw ? (float*)workspace : nullptr;
+    a.dwq = dq_weight;
+    a.dwk = dk_weight;
+    return launched(launch_norm_rope_bwd(a, (int32_t)dtype, (int32_t)rope->layout, (hipStream_t)stream));
+}
+
+tcm_status tcm_paged_attention_workspace(int64_t B, int64_t Hq, int64_t Hk, int64_t D,
+                                         int64_t max_len, int64_t* bytes) {
+    if (!bytes) return TCM_ERR_NULL_POINTER;
+    tcm_status s = check_attn_sizes(B, Hq, Hk, D, max_len);
+    if (s != TCM_OK) return s;
+    // enough for every call with these sizes and at most max_len (a shorter one
+    // may take more and smaller chunks)
+    int64_t n = 1;
+    if (Hk > 0) {
+        n = most_splits(B, Hq, Hk);
+        if (n > cdiv(max_len, kMinChunk)) n = cdiv(max_len, kMinChunk);
+    }
+    *bytes = attn_workspace(B, Hq, D, n);
+    return TCM_OK;
+}
+
+tcm_status tcm_paged_attention(const tcm_heads* q, const tcm_cache* cache,
+                               const int32_t* block_table, int64_t table_stride,
+                               const int32_t* lengths, int64_t max_len, const tcm_heads* out,
+                               float* lse, int64_t B, int64_t Hq, int64_t Hk, int64_t D,
+                               float scale, int64_t window, tcm_dtype dtype, void* workspace,
+                               int64_t workspace_bytes, void* stream) {
+    if (!half_type(dtype)) return TCM_ERR_UNSUPPORTED_DTYPE;
+    tcm_status s = check_attn_sizes(B, Hq, Hk, D, max_len);
+    if (s != TCM_OK) return s;
+    if (window < 0 || table_stride < 0) return TCM_ERR_INVALID_SHAPE;
+    if (table_stride > INT32_MAX) return TCM_ERR_UNSUPPORTED_SHAPE;
+    if ((s = check_cache(cache, dtype, Hk, D, false)) != TCM_OK) return s;
+    if (cache->dtype == TCM_E4M3 && D % 16 != 0) return TCM_ERR_MISALIGNED;
+    if (B == 0 || Hq == 0) return TCM_OK;
+    if (!lengths || (table_stride > 0 && !block_table)) return TCM_ERR_NULL_POINTER;
+    if ((s = check_heads(q)) != TCM_OK || (s = check_written(out, B, Hq, D)) != TCM_OK) return s;
+    // no page, no key
+    if (cache->pages == 0) max_len = 0;
+    // the first tile of a window begins up to 31 keys before it
+    const int64_t span = window > 0 && window + 31 < max_len ? window + 31 : max_len;
+    Split sp = split_of(B, Hq, Hk, span);
+    if (sp.n > 1) {
+        if (!workspace) return TCM_ERR_NULL_POINTER;
+        if (!aligned16(workspace)) return TCM_ERR_MISALIGNED;
+        if (workspace_bytes < attn_workspace(B, Hq, D, sp.n)) return TCM_ERR_WORKSPACE;
+    }
+    DeviceInfo dev;
+    if ((s = device_info(&dev)) != TCM_OK) return s;
+    AttnArgs a;
+    memset(&a, 0, sizeof(a));
+    const bool e4m3 = cache->dtype == TCM_E4M3;
+    const int64_t es = e4m3 ? 1 : 2;
+    a.q = view(q);
+    a.out = view(out);
+    a.kc = (const char*)cache->k;
+    a.vc = (const char*)cache->v;
+    a.k_page = cache->k_page_stride * es;
+    a.k_tok = cache->k_token_stride * es;
+    a.k_head = cache->k_head_stride * es;
+    a.v_page = cache->v_page_stride * es;
+    a.v_tok = cache->v_token_stride * es;
+    a.v_head = cache->v_head_stride * es;
+    a.table = block_table;
+    a.table_stride = table_stride;
+    a.lengths = lengths;
+    a.lse = lse;
+    a.po = (float*)workspace;
+    a.pml = a.po + B * Hq * sp.n * D;
+    a.B = (int32_t)B;
+    a.Hq = (int32_t)Hq;
+    a.Hk = (int32_t)Hk;
+    a.G = (int32_t)(Hq / Hk);
+    a.D = (int32_t)D;
+    a.pages = (int32_t)cache->pages;
+    a.page_size = (int32_t)cache->page_size;
+    a.page_shift = -1;
+    for (int i = 0; i <= 20; ++i)
+        if (cache->page_size == int64_t(1) << i) a.page_shift = i;
+    a.max_len = (int32_t)max_len;
+    a.window = window > max_len ? 0 : (int32_t)window;
+    a.chunk = (int32_t)sp.chunk;
+    a.splits = (int32_t)sp.n;
+    a.qblocks = (int32_t)cdiv(Hq / Hk, 16);
+    a.scale_log2 = scale * (e4m3 ? cache->k_scale : 1.0f) * 1.4426950408889634f;
+    a.v_scale = e4m3 ? cache->v_scale : 1.0f;
+    return launched(launch_paged_attention(a, (int32_t)dtype, e4m3, (hipStream_t)stream));
+}
+
+}  // extern "C"

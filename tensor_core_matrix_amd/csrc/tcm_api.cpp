@@ -11,6 +11,7 @@
 #include <hip/hip_runtime.h>
 
 #include "../../include/tcm.h"
+#include "tcm_host.h"
 #include "tcm_internal.h"
 
 namespace tcm {
@@ -43,25 +44,12 @@ VariantInfo variant_info(int32_t v) {
     return {0, 0, 0, 0, 0, 0, kThreads};
 }
 
-}  // namespace tcm
-
 namespace {
-
-using namespace tcm;
-
-constexpr int64_t kMaxK = int64_t(1) << 20;     // keeps buffer offsets within 32 bits
-constexpr int64_t kMaxMN = int64_t(1) << 30;    // row indices stay in int32
-constexpr int64_t kMaxLd = int64_t(1) << 21;    // operand leading dimensions (32-bit offsets)
 constexpr int kMaxDevices = 64;
-
-struct DeviceInfo {
-    int cus = 0;
-    bool gfx950 = false;
-    hipError_t err = hipSuccess;
-};
 
 DeviceInfo g_dev[kMaxDevices];
 std::once_flag g_dev_once[kMaxDevices];
+}  // namespace
 
 tcm_status device_info(DeviceInfo* out) {
     int dev = 0;
@@ -79,6 +67,16 @@ tcm_status device_info(DeviceInfo* out) {
     if (out->err != hipSuccess || !out->gfx950 || out->cus <= 0) return TCM_ERR_NO_DEVICE;
     return TCM_OK;
 }
+
+}  // namespace tcm
+
+namespace {
+
+using namespace tcm;
+
+constexpr int64_t kMaxK = int64_t(1) << 20;     // keeps buffer offsets within 32 bits
+constexpr int64_t kMaxMN = int64_t(1) << 30;    // row indices stay in int32
+constexpr int64_t kMaxLd = int64_t(1) << 21;    // operand leading dimensions (32-bit offsets)
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -715,6 +713,7 @@ const char* tcm_status_string(tcm_status s) {
     case TCM_ERR_HIP: return "TCM_ERR_HIP: a HIP runtime call or kernel launch failed";
     case TCM_ERR_INVALID_ARGUMENT:
         return "TCM_ERR_INVALID_ARGUMENT: an order or operation code outside its values";
+    case TCM_ERR_WORKSPACE: return "TCM_ERR_WORKSPACE: the workspace is smaller than the call needs";
     }
     return "TCM_ERR_UNKNOWN: unknown status code";
 }
