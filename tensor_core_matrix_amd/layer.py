@@ -26,6 +26,12 @@ _OUT = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
 _LAYOUTS = {"half": 0, "interleaved": 1}
 
 
+# The current stream's handle without making a Stream object (2 us a call, a third of a
+# small call's whole time on the host).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _half(t, what):
     code = _HALF.get(t.dtype)
     if code is None:
@@ -33,64 +39,66 @@ def _half(t, what):
     return code
 
 
-def _expect(t, what, shape, dtype, device):
-    """t as a dense tensor of this shape, type and device."""
-    if t.dtype != dtype:
+def _expect(t, what, shape, dtype, dev):
+    """t as a dense tensor of this shape, type and device (index): its address."""
+    if t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if t.device != device or not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous and on {device}")
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous and on the first tensor's device")
     return t.data_ptr()
 
 
-def _heads(t, what, T, H, D, dtype, device):
-    """The view (T, H, D) of t; its elements of a head must be contiguous."""
-    if t.dtype != dtype:
+def _heads(t, what, shape, dtype, dev):
+    """The view (tokens, heads, D) of t; the elements of a head must be contiguous."""
+    ts, hs, ds = t.stride() if t.dim() == 3 else (0, 0, 0)
+    if t.dtype is dtype and t.shape == shape and ds == 1 and t.get_device() == dev:
+        return Heads(t.data_ptr(), ts, hs)
+    if t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
-    if t.shape != (T, H, D):
-        raise ValueError(f"{what} must have shape {(T, H, D)}, not {tuple(t.shape)}")
-    ts, hs, ds = t.stride()
-    if t.device != device or (ds != 1 and D > 1):
-        raise ValueError(f"{what} must have contiguous heads and be on {device}")
-    return Heads(t.data_ptr(), ts, hs)
+    if t.shape != shape:
+        raise ValueError(f"{what} must have shape {shape}, not {tuple(t.shape)}")
+    raise ValueError(f"{what} must have contiguous heads and be on the first tensor's device")
 
 
-def _cache(k, v, k_scale, v_scale, Hk, D, dtype, device):
-    if k.dtype != v.dtype or k.shape != v.shape or k.dim() != 4 or k.shape[2:] != (Hk, D):
+def _cache(k, v, k_scale, v_scale, Hk, D, dtype, dev):
+    shape = k.shape
+    if k.dtype is not v.dtype or shape != v.shape or len(shape) != 4 or shape[2] != Hk or shape[3] != D:
         raise ValueError(f"k_cache and v_cache must be (pages, page_size, {Hk}, {D}) of one type")
-    if k.dtype == dtype:
+    if k.dtype is dtype:
         code = _HALF[dtype]
     elif k.dtype in (torch.float8_e4m3fn, torch.uint8):
         code = E4M3
     else:
         raise TypeError(f"a cache is {dtype}, float8_e4m3fn or uint8 (E4M3 bytes), not {k.dtype}")
-    ks, vs = k.stride(), v.stride()
-    if k.device != device or v.device != device or (D > 1 and (ks[3] != 1 or vs[3] != 1)):
-        raise ValueError(f"caches must have contiguous heads and be on {device}")
-    return Cache(k.data_ptr(), v.data_ptr(), k.shape[0], k.shape[1], ks[0], ks[1], ks[2], vs[0],
-                 vs[1], vs[2], code, k_scale, v_scale)
+    kp, kt, kh, ke = k.stride()
+    vp, vt, vh, ve = v.stride()
+    if ke != 1 or ve != 1 or k.get_device() != dev or v.get_device() != dev:
+        raise ValueError("caches must have contiguous heads and be on the first tensor's device")
+    return Cache(k.data_ptr(), v.data_ptr(), shape[0], shape[1], kp, kt, kh, vp, vt, vh, code, k_scale,
+                 v_scale)
 
 
-def _rope(T, D, positions, inv_freq, wq, wk, eps, layout, factor, norm, dtype, device):
+def _rope(T, D, positions, inv_freq, wq, wk, eps, layout, factor, norm, dtype, dev):
     rot = 2 * inv_freq.shape[0] if inv_freq is not None else 0
-    pos = freq = None
+    pos = freq = a = b = None
     if rot:
-        pos = _expect(positions, "positions", (T,), torch.int32, device)
-        freq = _expect(inv_freq, "inv_freq", (rot // 2,), torch.float64, device)
-    if layout not in _LAYOUTS:
+        pos = _expect(positions, "positions", (T,), torch.int32, dev)
+        freq = _expect(inv_freq, "inv_freq", (rot // 2,), torch.float64, dev)
+    kind = _LAYOUTS.get(layout)
+    if kind is None:
         raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}, not {layout!r}")
-    wt = dtype
-    for w in (wq, wk):
-        if w is not None:
-            if not norm:
-                raise ValueError("weights belong to the norm: norm=False takes none")
-            wt = w.dtype
-    if wt not in (dtype, torch.float32):
+    wt = wk.dtype if wk is not None else wq.dtype if wq is not None else dtype
+    if not norm and (wq is not None or wk is not None):
+        raise ValueError("weights belong to the norm: norm=False takes none")
+    if wt is not dtype and wt is not torch.float32:
         raise TypeError(f"weights must be {dtype} or float32, not {wt}")
-    a = None if wq is None else _expect(wq, "wq", (D,), wt, device)
-    b = None if wk is None else _expect(wk, "wk", (D,), wt, device)
-    return Rope(D, rot, pos, freq, factor, _LAYOUTS[layout], 1 if norm else 0, eps, a, b, _OUT[wt])
+    if wq is not None:
+        a = _expect(wq, "wq", (D,), wt, dev)
+    if wk is not None:
+        b = _expect(wk, "wk", (D,), wt, dev)
+    return Rope(D, rot, pos, freq, factor, kind, 1 if norm else 0, eps, a, b, _OUT[wt])
 
 
 def _bytes(f, *sizes):
@@ -99,26 +107,32 @@ def _bytes(f, *sizes):
     return n.value
 
 
-def _workspace(ws, need, device):
-    """(pointer, bytes, the tensor) of a workspace of `need` bytes."""
+def _workspace(ws, dev, size, *sizes):
+    """(pointer, bytes, the tensor) of the given workspace, or of a new one of
+    size(*sizes) bytes."""
+    if dev < 0:
+        raise ValueError("tensors must be on a GPU")
     if ws is None:
+        need = size(*sizes)
         if need == 0:
             return None, 0, None
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
-    elif ws.device != device or not ws.is_contiguous():
-        raise ValueError(f"workspace must be contiguous and on {device}")
+        ws = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", dev))
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("workspace must be contiguous and on the first tensor's device")
     return ws.data_ptr(), ws.numel() * ws.element_size(), ws
 
 
-def _run(device, f, *args):
+def _run(dev, f, *args):
     """f(*args, stream) on the device's current stream."""
-    if device.type != "cuda":
-        raise ValueError(f"tensors must be on a GPU, not on {device}")
-    if device.index == torch.cuda.current_device():
-        _check(f(*args, torch.cuda.current_stream(device).cuda_stream))
+    if dev < 0:
+        raise ValueError("tensors must be on a GPU")
+    if dev == torch.cuda.current_device():
+        status = f(*args, _raw_stream(dev))
     else:
-        with torch.cuda.device(device):
-            _check(f(*args, torch.cuda.current_stream(device).cuda_stream))
+        with torch.cuda.device(dev):
+            status = f(*args, _raw_stream(dev))
+    if status:
+        _check(status)
 
 
 def lora_workspace(M, K, R):
@@ -135,7 +149,7 @@ def lora_gemm_tn(x, w, lora_a, lora_b, row_adapter, scales=None, ranks=None, out
     int32: only the first ranks[a] rows of lora_a[a] and columns of lora_b[a]
     are used; out (M, N) of x's type or float32, with contiguous rows."""
     code = _half(x, "x")
-    dev = x.device
+    dev = x.get_device()
     M, K = x.shape
     N = w.shape[0]
     L, R = lora_a.shape[:2]
@@ -146,10 +160,10 @@ def lora_gemm_tn(x, w, lora_a, lora_b, row_adapter, scales=None, ranks=None, out
     sp = None if scales is None else _expect(scales, "scales", (L,), torch.float32, dev)
     kp = None if ranks is None else _expect(ranks, "ranks", (L,), torch.int32, dev)
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype or x.dtype, device=dev)
-    elif out.shape != (M, N) or out.device != dev:
-        raise ValueError(f"out must be {(M, N)} on {dev}")
-    if out.dtype != x.dtype and out.dtype != torch.float32:
+        out = torch.empty((M, N), dtype=out_dtype or x.dtype, device=x.device)
+    elif out.shape != (M, N) or out.get_device() != dev:
+        raise ValueError(f"out must be {(M, N)} on the first tensor's device")
+    if out.dtype is not x.dtype and out.dtype is not torch.float32:
         raise TypeError(f"out must be {x.dtype} or float32, not {out.dtype}")
     xs, os = x.stride(), out.stride()
     if (K > 1 and xs[1] != 1) or (N > 1 and os[1] != 1):
@@ -158,7 +172,7 @@ def lora_gemm_tn(x, w, lora_a, lora_b, row_adapter, scales=None, ranks=None, out
     ldo = os[0] if M > 1 else max(os[0], N, 1)
     if M <= 1 and ldx % 8:
         ldx = max(K, 1)
-    ws, nbytes, keep = _workspace(workspace, 0 if workspace is not None else lora_workspace(M, K, R), dev)
+    ws, nbytes, keep = _workspace(workspace, dev, lora_workspace, M, K, R)
     _run(dev, lib().tcm_lora_gemm_tn, x.data_ptr(), ldx, wp, ap, bp, rp, kp, sp, out.data_ptr(), ldo,
          M, N, K, L, R, code, _OUT[out.dtype], ws, nbytes)
     return out
@@ -174,17 +188,18 @@ def qk_norm_rope(q, k, positions, inv_freq, wq=None, wk=None, eps=1e-6, layout="
     "interleaved" (2j, 2j + 1); wq, wk (D,) of q's type or float32.  q_out may be q
     and k_out k."""
     code = _half(q, "q")
-    dev = q.device
+    dev, dt = q.get_device(), q.dtype
     T, Hq, D = q.shape
     Hk = k.shape[1]
+    qs, ks = (T, Hq, D), (T, Hk, D)
     if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
+        q_out = torch.empty(qs, dtype=dt, device=q.device)
     if k_out is None:
-        k_out = torch.empty((T, Hk, D), dtype=q.dtype, device=dev)
-    r = _rope(T, D, positions, inv_freq, wq, wk, eps, layout, factor, norm, q.dtype, dev)
-    _run(dev, lib().tcm_qk_norm_rope, _heads(q, "q", T, Hq, D, q.dtype, dev),
-         _heads(k, "k", T, Hk, D, q.dtype, dev), _heads(q_out, "q_out", T, Hq, D, q.dtype, dev),
-         _heads(k_out, "k_out", T, Hk, D, q.dtype, dev), T, Hq, Hk, r, code)
+        k_out = torch.empty(ks, dtype=dt, device=q.device)
+    r = _rope(T, D, positions, inv_freq, wq, wk, eps, layout, factor, norm, dt, dev)
+    _run(dev, lib().tcm_qk_norm_rope, _heads(q, "q", qs, dt, dev),
+         _heads(k, "k", ks, dt, dev), _heads(q_out, "q_out", qs, dt, dev),
+         _heads(k_out, "k_out", ks, dt, dev), T, Hq, Hk, r, code)
     return q_out, k_out
 
 
@@ -197,16 +212,17 @@ def qk_norm_rope_cache(q, k, v, positions, inv_freq, k_cache, v_cache, slots, wq
     of q's type, or E4M3 (float8_e4m3fn or uint8), which holds k / k_scale and
     v / v_scale."""
     code = _half(q, "q")
-    dev = q.device
+    dev, dt = q.get_device(), q.dtype
     T, Hq, D = q.shape
     Hk = k.shape[1]
+    qs, ks = (T, Hq, D), (T, Hk, D)
     if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
-    r = _rope(T, D, positions, inv_freq, wq, wk, eps, layout, factor, norm, q.dtype, dev)
-    _run(dev, lib().tcm_qk_norm_rope_cache, _heads(q, "q", T, Hq, D, q.dtype, dev),
-         _heads(k, "k", T, Hk, D, q.dtype, dev), _heads(v, "v", T, Hk, D, q.dtype, dev),
-         _heads(q_out, "q_out", T, Hq, D, q.dtype, dev),
-         _cache(k_cache, v_cache, k_scale, v_scale, Hk, D, q.dtype, dev),
+        q_out = torch.empty(qs, dtype=dt, device=q.device)
+    r = _rope(T, D, positions, inv_freq, wq, wk, eps, layout, factor, norm, dt, dev)
+    _run(dev, lib().tcm_qk_norm_rope_cache, _heads(q, "q", qs, dt, dev),
+         _heads(k, "k", ks, dt, dev), _heads(v, "v", ks, dt, dev),
+         _heads(q_out, "q_out", qs, dt, dev),
+         _cache(k_cache, v_cache, k_scale, v_scale, Hk, D, dt, dev),
          _expect(slots, "slots", (T,), torch.int32, dev), T, Hq, Hk, r, code)
     return q_out
 
@@ -223,30 +239,30 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, positions, inv_freq, wq=None, wk=None
     those of its outputs; q, k and the rest as given to it.  dwq, dwk (D,) float32
     are computed for the weights that are given (else None)."""
     code = _half(q, "q")
-    dev = q.device
+    dev, dt = q.get_device(), q.dtype
     T, Hq, D = q.shape
     Hk = k.shape[1]
+    qs, ks = (T, Hq, D), (T, Hk, D)
     if dq is None:
-        dq = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
+        dq = torch.empty(qs, dtype=dt, device=q.device)
     if dk is None:
-        dk = torch.empty((T, Hk, D), dtype=q.dtype, device=dev)
-    r = _rope(T, D, positions, inv_freq, wq, wk, eps, layout, factor, norm, q.dtype, dev)
+        dk = torch.empty(ks, dtype=dt, device=q.device)
+    r = _rope(T, D, positions, inv_freq, wq, wk, eps, layout, factor, norm, dt, dev)
     if wq is None:
         dwq = None
     elif dwq is None:
-        dwq = torch.empty((D,), dtype=torch.float32, device=dev)
+        dwq = torch.empty((D,), dtype=torch.float32, device=q.device)
     if wk is None:
         dwk = None
     elif dwk is None:
-        dwk = torch.empty((D,), dtype=torch.float32, device=dev)
+        dwk = torch.empty((D,), dtype=torch.float32, device=q.device)
     ws = nbytes = keep = None
     if dwq is not None or dwk is not None:
-        need = 0 if workspace is not None else qk_norm_rope_bwd_workspace(D)
-        ws, nbytes, keep = _workspace(workspace, need, dev)
-    _run(dev, lib().tcm_qk_norm_rope_bwd, _heads(dq_out, "dq_out", T, Hq, D, q.dtype, dev),
-         _heads(dk_out, "dk_out", T, Hk, D, q.dtype, dev), _heads(q, "q", T, Hq, D, q.dtype, dev),
-         _heads(k, "k", T, Hk, D, q.dtype, dev), _heads(dq, "dq", T, Hq, D, q.dtype, dev),
-         _heads(dk, "dk", T, Hk, D, q.dtype, dev),
+        ws, nbytes, keep = _workspace(workspace, dev, qk_norm_rope_bwd_workspace, D)
+    _run(dev, lib().tcm_qk_norm_rope_bwd, _heads(dq_out, "dq_out", qs, dt, dev),
+         _heads(dk_out, "dk_out", ks, dt, dev), _heads(q, "q", qs, dt, dev),
+         _heads(k, "k", ks, dt, dev), _heads(dq, "dq", qs, dt, dev),
+         _heads(dk, "dk", ks, dt, dev),
          None if dwq is None else _expect(dwq, "dwq", (D,), torch.float32, dev),
          None if dwk is None else _expect(dwk, "dwk", (D,), torch.float32, dev), T, Hq, Hk, r, code, ws,
          nbytes or 0)
@@ -270,25 +286,23 @@ def paged_attention(q, k_cache, v_cache, block_table, lengths, scale=None, windo
     without keys gives zeros.  lse (B, Hq) float32 takes the logarithm of the sum
     of exponentials (-inf without keys).  out may be q."""
     code = _half(q, "q")
-    dev = q.device
-    B, Hq, D = q.shape
-    page_size, Hk = k_cache.shape[1:3]
+    dev, dt = q.get_device(), q.dtype
+    qs = B, Hq, D = tuple(q.shape)
+    _, page_size, Hk, _ = k_cache.shape
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=q.dtype, device=dev)
-    if block_table.dim() != 2 or block_table.shape[0] != B or block_table.dtype != torch.int32:
+        out = torch.empty(qs, dtype=dt, device=q.device)
+    if block_table.dim() != 2 or block_table.shape[0] != B or block_table.dtype is not torch.int32:
         raise ValueError(f"block_table must be ({B}, pages of a sequence) int32")
     per, (ts, es) = block_table.shape[1], block_table.stride()
-    if block_table.device != dev or (per > 1 and es != 1) or (B > 1 and ts < per):
-        raise ValueError(f"block_table must have contiguous rows and be on {dev}")
-    if max_len is None:
+    if block_table.get_device() != dev or (per > 1 and es != 1) or (B > 1 and ts < per):
+        raise ValueError("block_table must have contiguous rows and be on the first tensor's device")
+    if max_len is None or max_len > per * page_size:
         max_len = per * page_size
-    max_len = min(max_len, per * page_size)
-    ws, nbytes, keep = _workspace(
-        workspace, 0 if workspace is not None else paged_attention_workspace(B, Hq, Hk, D, max_len), dev)
-    _run(dev, lib().tcm_paged_attention, _heads(q, "q", B, Hq, D, q.dtype, dev),
-         _cache(k_cache, v_cache, k_scale, v_scale, Hk, D, q.dtype, dev), block_table.data_ptr(),
+    cache = _cache(k_cache, v_cache, k_scale, v_scale, Hk, D, dt, dev)
+    ws, nbytes, keep = _workspace(workspace, dev, paged_attention_workspace, B, Hq, Hk, D, max_len)
+    _run(dev, lib().tcm_paged_attention, _heads(q, "q", qs, dt, dev), cache, block_table.data_ptr(),
          ts if B > 1 and per else per, _expect(lengths, "lengths", (B,), torch.int32, dev), max_len,
-         _heads(out, "out", B, Hq, D, q.dtype, dev),
+         _heads(out, "out", qs, dt, dev),
          None if lse is None else _expect(lse, "lse", (B, Hq), torch.float32, dev), B, Hq, Hk, D,
          D ** -0.5 if scale is None else scale, window, code, ws, nbytes)
     return out
