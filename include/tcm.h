@@ -369,7 +369,8 @@ typedef struct tcm_heads {
  * the type of the calls that use it, or TCM_E4M3, which stands for
  * k_scale * element and v_scale * element (the scales are not looked at
  * otherwise).  16-byte aligned, strides whole 16-byte pieces
- * (TCM_ERR_MISALIGNED); page_size at most 2^20. */
+ * (TCM_ERR_MISALIGNED); page_size at most 2^20 and token strides at most 2^25
+ * elements (TCM_ERR_UNSUPPORTED_SHAPE). */
 typedef struct tcm_cache {
     void* k;
     void* v;

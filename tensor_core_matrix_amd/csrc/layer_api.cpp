@@ -23,6 +23,9 @@ constexpr int64_t kMaxHeads = 65535;
 // a stride (elements) and its product with a count stay far from 64 bits
 constexpr int64_t kMaxStride = int64_t(1) << 40;
 
+// 16 tokens of a page stay within 32 bits of bytes
+constexpr int64_t kMaxTokenStride = int64_t(1) << 25;
+
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -78,7 +81,9 @@ tcm_status check_cache(const tcm_cache* c, tcm_dtype dtype, int64_t Hk, int64_t 
         }
     }
     if (c->pages > 0 && (!c->k || !c->v)) return TCM_ERR_NULL_POINTER;
-    if (c->pages > INT32_MAX || c->page_size > (int64_t(1) << 20)) return TCM_ERR_UNSUPPORTED_SHAPE;
+    if (c->pages > INT32_MAX || c->page_size > (int64_t(1) << 20) || c->k_token_stride > kMaxTokenStride ||
+        c->v_token_stride > kMaxTokenStride)
+        return TCM_ERR_UNSUPPORTED_SHAPE;
     const int64_t piece = c->dtype == TCM_E4M3 ? 16 : 8;
     for (int64_t s : st)
         if (s % piece != 0) return TCM_ERR_MISALIGNED;
@@ -126,23 +131,45 @@ int64_t bwd_workspace(int64_t D) { return int64_t(kRopeBwdGrid) * 2 * D * 4; }
 
 // ---- paged attention ----------------------------------------------------------------
 
-// The split over the length: chunks (of whole 128-key rounds of a workgroup)
-// such that about 1024 workgroups share the work, four for every compute unit,
-// but none with fewer than 256 keys.
-constexpr int64_t kMinChunk = 256;
+// The split over the length.  Two ways to deal the work to workgroups of four waves:
+//  * heads == 1: a chunk of one key-value head's keys, its tiles dealt to the
+//    waves.  Chunks of 1024 keys, or fewer (256 at least) where that leaves fewer than
+//    1024 workgroups: 64 sequences of up to 4096 keys take 101 us in chunks of 1024,
+//    102 of 768 and 115 of 2048 (lengths differ: the last chunks idle the device);
+//    32 of up to 8192 E4M3 keys 67, and 72 in chunks of 512 (each pays its first
+//    reads' latency).
+//  * heads == 4: the same chunk of four heads, one a wave, so that the
+//    workgroup reads whole stretches of memory (a probe that only reads reaches
+//    6.9 TB/s that way and 6.4 with a head a workgroup).  One sequence of 131001
+//    keys takes 87 us, and 93 the other way; 64 of different lengths 106.  So it
+//    is for few sequences with work for every compute unit.
+constexpr int64_t kMinChunk = 256, kChunk = 1024;
 struct Split {
-    int64_t chunk, n;
+    int64_t chunk, n, heads;
 };
-int64_t most_splits(int64_t B, int64_t Hq, int64_t Hk) {
+int64_t split_units(int64_t B, int64_t Hq, int64_t Hk) {
     const int64_t units = B * Hk * cdiv(Hq / Hk, 16);
-    const int64_t n = cdiv(1024, units > 0 ? units : 1);
-    return n < kAttnMaxSplits ? n : kAttnMaxSplits;
+    return units > 0 ? units : 1;
 }
 Split split_of(int64_t B, int64_t Hq, int64_t Hk, int64_t span) {
-    int64_t chunk = cdiv(cdiv(span, most_splits(B, Hq, Hk)), 128) * 128;
-    if (chunk < kMinChunk) chunk = kMinChunk;
-    const int64_t n = cdiv(span, chunk);
-    return {chunk, n > 0 ? n : 1};
+    Split s;
+    s.heads = Hk % 4 == 0 && B <= 4 && B * (Hk / 4) * cdiv(span, kChunk) >= 256 ? 4 : 1;
+    s.chunk = kChunk;
+    if (s.heads == 1) {
+        const int64_t c = cdiv(cdiv(span, cdiv(1024, split_units(B, Hq, Hk))), 128) * 128;
+        s.chunk = c < kMinChunk ? kMinChunk : c < kChunk ? c : kChunk;
+    }
+    if (cdiv(span, s.chunk) > kAttnMaxSplits) s.chunk = cdiv(cdiv(span, kAttnMaxSplits), 128) * 128;
+    s.n = cdiv(span, s.chunk);
+    if (s.n < 1) s.n = 1;
+    return s;
+}
+// No split_of() with these sizes and at most this span has more chunks.
+int64_t most_splits(int64_t B, int64_t Hq, int64_t Hk, int64_t span) {
+    int64_t n = cdiv(1024, split_units(B, Hq, Hk));
+    if (n < cdiv(span, kChunk)) n = cdiv(span, kChunk);
+    if (n > cdiv(span, kMinChunk)) n = cdiv(span, kMinChunk);
+    return n < kAttnMaxSplits ? n : kAttnMaxSplits;
 }
 int64_t attn_workspace(int64_t B, int64_t Hq, int64_t D, int64_t n) {
     return n > 1 ? B * Hq * n * (D + 2) * 4 : 0;
@@ -347,13 +374,7 @@ tcm_status tcm_paged_attention_workspace(int64_t B, int64_t Hq, int64_t Hk, int6
     if (!bytes) return TCM_ERR_NULL_POINTER;
     tcm_status s = check_attn_sizes(B, Hq, Hk, D, max_len);
     if (s != TCM_OK) return s;
-    // enough for every call with these sizes and at most max_len (a shorter one
-    // may take more and smaller chunks)
-    int64_t n = 1;
-    if (Hk > 0) {
-        n = most_splits(B, Hq, Hk);
-        if (n > cdiv(max_len, kMinChunk)) n = cdiv(max_len, kMinChunk);
-    }
+    const int64_t n = Hk > 0 ? most_splits(B, Hq, Hk, max_len) : 1;
     *bytes = attn_workspace(B, Hq, D, n);
     return TCM_OK;
 }
@@ -420,6 +441,7 @@ tcm_status tcm_paged_attention(const tcm_heads* q, const tcm_cache* cache,
     a.window = window > max_len ? 0 : (int32_t)window;
     a.chunk = (int32_t)sp.chunk;
     a.splits = (int32_t)sp.n;
+    a.heads = (int32_t)sp.heads;
     a.qblocks = (int32_t)cdiv(Hq / Hk, 16);
     a.scale_log2 = scale * (e4m3 ? cache->k_scale : 1.0f) * 1.4426950408889634f;
     a.v_scale = e4m3 ? cache->v_scale : 1.0f;

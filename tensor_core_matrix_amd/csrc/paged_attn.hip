@@ -70,21 +70,36 @@ __device__ __forceinline__ void load_words(const char* p, uint32_t* w) {
     typedef typename Bytes<B>::type v_t;
 #pragma unroll
     for (int i = 0; i < N * 4 / B; ++i) {
-        const v_t v = *(const v_t*)(p + i * B);
+        const v_t v = __builtin_nontemporal_load((const v_t*)(p + i * B));
 #pragma unroll
         for (int j = 0; j < B / 4; ++j) w[i * (B / 4) + j] = v[j];
     }
 }
 
-// The keys [lo, end) of sequence b that chunk c covers, and the whole range's
-// first tile.
+// An int32 at a wave-uniform address that no kernel of the call writes, read
+// through the scalar cache: its wait is apart from the vector loads', so a page's
+// number can be looked up while a tile is on its way.
+__device__ __forceinline__ int scalar_int(const int32_t* p) {
+    return *(const __attribute__((address_space(4))) int32_t*)p;
+}
+
+// The larger of x and of lane l ^ 16's, and then of lane l ^ 32's, by register
+// exchanges between rows of 16 and halves of the wave (no trip through LDS).
+__device__ __forceinline__ float max_over_groups(float x) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+
+// The keys [lo, len) of sequence b, and where the first tile begins.
 struct Range {
     int base, lo, len;
 };
 __device__ __forceinline__ Range range_of(const AttnArgs& p, int b) {
     Range r;
     const int64_t room = p.table_stride * (int64_t)p.page_size;
-    int len = p.lengths[b];
+    int len = scalar_int(p.lengths + b);
     len = len < 0 ? 0 : len;
     len = min(len, p.max_len);
     if (len > room) len = (int)room;
@@ -98,25 +113,40 @@ __device__ __forceinline__ Range range_of(const AttnArgs& p, int b) {
 // bytes.  ALIGNED: page_size is a multiple of 16, so the 16 keys of a half
 // tile lie in one page, whose number is looked up once.
 template <class T, int DP, bool E4M3, bool ALIGNED>
-__global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attn_kernel(AttnArgs p) {
+__global__ __launch_bounds__(256, DP == 256 ? 1 : DP == 128 && E4M3 && ALIGNED ? 3 : 2) void attn_kernel(AttnArgs p) {
     typedef Half16<T> H;
     typedef typename H::x8 x8;
     constexpr int ES = E4M3 ? 1 : 2;
     constexpr int STEPS = DP / 32;          // products of 32 over the head
     constexpr int VE = DP / 16;             // elements of a value row a lane holds
-    constexpr int KW = E4M3 ? 2 : 4;        // words of a lane's 8 key elements
     constexpr int VW = VE * ES / 4;         // words of a lane's piece of a value row
-    __shared__ __attribute__((aligned(16))) float lo_[4][16][DP + 4];
+    constexpr int KB = DP * ES;             // bytes of a key
+    constexpr int KL = KB / 16;             // lanes that read a key,
+    constexpr int KN = 64 / KL;             // keys of one read
+    constexpr int KI = 32 / KN;             // and reads of a tile
+    // the tile's keys, one area a wave; at the end the waves' results
+    constexpr int OB = 4 * 16 * (DP + 4) * 4, KA = 32 * KB;
+    __shared__ __attribute__((aligned(1024))) char lds[OB > 4 * KA ? OB : 4 * KA];
+    float (*const lo_)[16][DP + 4] = (float (*)[16][DP + 4])lds;
     __shared__ float lm_[4][16], ll_[4][16];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r16 = lane & 15, g4 = lane >> 4;
-    const int b = blockIdx.z;
-    const int hk = blockIdx.y / p.qblocks, qb = blockIdx.y - hk * p.qblocks;
+    // Chunk by chunk over all sequences and key-value heads.  Workgroups are dealt
+    // to the 8 XCDs in turn, so a sequence's next chunk is moved on by one: were
+    // the chunk's number the XCD's (or the sequence's, for a count of sequences
+    // that 8 divides), the XCD of the last chunks would idle.
+    const int groups = p.Hk / p.heads;  // of key-value heads
+    const int units = p.B * groups, per = units * p.qblocks;
+    const int split = blockIdx.x / per, rest = blockIdx.x - split * per;
+    const int qb = rest / units, unit = (rest - qb * units + split) % units;
+    const int b = unit / groups, hw = wave & (p.heads - 1), kw = wave / p.heads;
+    const int hk = (unit - b * groups) * p.heads + hw;
+    const int round = 128 / p.heads;  // keys of a round of the workgroup's waves
     const int h0 = hk * p.G + qb * 16, nh = min(16, p.G - qb * 16);
     const Range rg = range_of(p, b);
-    const int start = rg.base + (int)blockIdx.x * p.chunk;
+    const int start = rg.base + split * p.chunk;
     const int end = (int)min((int64_t)rg.len, (int64_t)start + p.chunk);
     if (p.splits > 1 && start >= end) return;
 
@@ -136,9 +166,9 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attn_kernel(AttnArgs p
         }
     }
 
-    // Pages and places of a tile's keys.  ALIGNED: one page and first place per
-    // 16 keys.  Otherwise lane l looks up key l % 32 and the others ask it.
-    // An unusable key (outside [lo, end), or in a hole) gets page -1.
+    // Pages and places of a tile's keys.  ALIGNED: the page of each 16 keys, in
+    // scalar registers.  Otherwise lane l has that of key l % 32 and the others ask
+    // it.  An unusable key (outside [lo, end), or in a hole) gets page -1.
     struct Where {
         int page[ALIGNED ? 2 : 1];
         int at[ALIGNED ? 2 : 1];
@@ -156,76 +186,84 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attn_kernel(AttnArgs p
             for (int h = 0; h < 2; ++h) {
                 const int key = key0 + 16 * h;
                 const int i = page_of(key, w.at[h]);
-                w.page[h] = key < end ? trow[i] : -1;
-                if ((uint32_t)w.page[h] >= (uint32_t)p.pages) w.page[h] = -1;
+                w.page[h] = key < end ? scalar_int(trow + i) : -1;
             }
         } else {
             const int key = key0 + (lane & 31);
             const int i = page_of(key, w.at[0]);
             w.page[0] = key >= rg.lo && key < end ? trow[i] : -1;
-            if ((uint32_t)w.page[0] >= (uint32_t)p.pages) w.page[0] = -1;
         }
         return w;
     };
+    auto settle = [&](Where& w) {
+#pragma unroll
+        for (int h = 0; h < (ALIGNED ? 2 : 1); ++h)
+            if ((uint32_t)w.page[h] >= (uint32_t)p.pages) w.page[h] = -1;
+    };
 
-    struct Tile {
-        uint32_t k[2][STEPS][KW];
+    struct Keys {
+        uint32_t k[KI][4];
+    };
+    struct Values {
         uint32_t v[8][VW];
     };
+    // A key's 16-byte piece c lies in LDS at c ^ swz(key): the 16 keys of one operand
+    // read then meet 16 different groups of banks.
+    constexpr int SH = KL >= 16 ? 0 : KL == 8 ? 1 : 2;
+    auto swz = [](int key) { return (key >> SH) & ((KL < 16 ? KL : 16) - 1); };
+    char* const ka = lds + wave * KA;
+    const int kc = lane % KL, kr = lane / KL;
+    // D < DP: pieces of a key past its end are zeros that nothing overwrites; lanes
+    // past the end of a value row read its beginning for elements nobody stores
+    const bool kin = kc * (16 / ES) < p.D;
+    if (!kin)
+#pragma unroll
+        for (int i = 0; i < KI; ++i)
+            *(i32x4_t*)(ka + (i * KN + kr) * KB + (kc ^ swz(i * KN + kr)) * 16) = (i32x4_t){};
+    const int vc = r16 * VE < p.D ? r16 * VE * ES : 0;
+    // ALIGNED: a lane's offsets from the first of 16 keys (16 token strides are
+    // less than 2^31 bytes)
+    const uint32_t koff = (uint32_t)kr * (uint32_t)p.k_tok + kc * 16;
+    const uint32_t voff = (uint32_t)(4 * g4) * (uint32_t)p.v_tok + vc;
     const char* const kh = p.kc + hk * p.k_head;
     const char* const vh = p.vc + hk * p.v_head;
-    const bool whole = p.D == DP;
     // the keys of inner positions 0..7 of this lane in the second product
     auto vkey = [&](int j) { return (j < 4 ? 0 : 16) + 4 * g4 + (j & 3); };
-    auto load = [&](Tile& t, const Where& w) {
+    auto load_keys = [&](Keys& t, const Where& w) {
+        if constexpr (ALIGNED) {
+            const char* kb[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            int page, at;
-            if constexpr (ALIGNED) {
-                page = max(w.page[h], 0);
-                at = w.at[h] + r16;
-            } else {
-                page = max(__shfl(w.page[0], r16 + 16 * h), 0);
-                at = __shfl(w.at[0], r16 + 16 * h);
-            }
-            const char* row = kh + page * p.k_page + at * p.k_tok;
-            if constexpr (E4M3) {
+            for (int h = 0; h < 2; ++h) kb[h] = kh + max(w.page[h], 0) * p.k_page + w.at[h] * p.k_tok;
+            if (kin)
 #pragma unroll
-                for (int s = 0; s < STEPS; s += 2) {
-                    uint32_t w4[4] = {0, 0, 0, 0};
-                    if (whole || elem(s) < p.D) load_words<4>(row + elem(s), w4);
-                    t.k[h][s][0] = w4[0], t.k[h][s][1] = w4[1];
-                    t.k[h][s + 1][0] = w4[2], t.k[h][s + 1][1] = w4[3];
+                for (int i = 0; i < KI; ++i) {
+                    constexpr int HALF = 16 / KN;  // reads of 16 keys
+                    load_words<4>(kb[i / HALF] + (i % HALF) * KN * p.k_tok + koff, t.k[i]);
                 }
-            } else {
+        } else {
+            const char* krow[KI];
 #pragma unroll
-                for (int s = 0; s < STEPS; ++s) {
-                    if (whole || elem(s) < p.D) {
-                        load_words<4>(row + 2 * elem(s), t.k[h][s]);
-                    } else {
+            for (int i = 0; i < KI; ++i)
+                krow[i] = kh + max(__shfl(w.page[0], i * KN + kr), 0) * p.k_page +
+                          __shfl(w.at[0], i * KN + kr) * p.k_tok + kc * 16;
+            if (kin)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) t.k[h][s][i] = 0;
-                    }
-                }
-            }
+                for (int i = 0; i < KI; ++i) load_words<4>(krow[i], t.k[i]);
         }
+    };
+    auto load_values = [&](Values& t, const Where& w) {
+        if constexpr (ALIGNED) {
+            const char* vb[2];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            int page, at;
-            if constexpr (ALIGNED) {
-                page = max(w.page[j >> 2], 0);
-                at = w.at[j >> 2] + 4 * g4 + (j & 3);
-            } else {
-                page = max(__shfl(w.page[0], vkey(j)), 0);
-                at = __shfl(w.at[0], vkey(j));
-            }
-            const char* row = vh + page * p.v_page + at * p.v_tok;
-            if (whole || r16 * VE < p.D) {
-                load_words<VW>(row + r16 * VE * ES, t.v[j]);
-            } else {
+            for (int h = 0; h < 2; ++h) vb[h] = vh + max(w.page[h], 0) * p.v_page + w.at[h] * p.v_tok;
 #pragma unroll
-                for (int i = 0; i < VW; ++i) t.v[j][i] = 0;
-            }
+            for (int j = 0; j < 8; ++j) load_words<VW>(vb[j >> 2] + (j & 3) * p.v_tok + voff, t.v[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                load_words<VW>(vh + max(__shfl(w.page[0], vkey(j)), 0) * p.v_page +
+                                   __shfl(w.at[0], vkey(j)) * p.v_tok + vc,
+                               t.v[j]);
         }
     };
 
@@ -234,7 +272,8 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attn_kernel(AttnArgs p
     for (int m = 0; m < VE; ++m) o[m] = (f32x4_t){};
     float mx = kNegInf, sum = 0.0f;
 
-    auto compute = [&](Tile& t, const Where& w, int key0) {
+    // (`next` asks for the next tile's keys, once the registers of these are free)
+    auto compute = [&](Keys& kt, Values& t, const Where& w, int key0, auto&& next) {
         // a tile with unusable keys: their scores become -infinity and, since a
         // probability of 0 times what lies in such a place may be NaN, their
         // values 0
@@ -252,30 +291,48 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attn_kernel(AttnArgs p
                 return __shfl(w.page[0], k32) >= 0;
             }
         };
+        // the keys through LDS, from whole rows into the operand's 16 keys x 16 bytes
+        // (the wave's own area: its LDS operations run in order)
+        wave_lds_exchange();
+        if (kin)
+#pragma unroll
+            for (int i = 0; i < KI; ++i) {
+                const int key = i * KN + kr;
+                *(i32x4_t*)(ka + key * KB + (kc ^ swz(key)) * 16) = *(i32x4_t*)kt.k[i];
+            }
+        wave_lds_exchange();
+        next();
         f32x4_t s[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             s[h] = (f32x4_t){};
+            const char* row = ka + (16 * h + r16) * KB;
+            const int sw = swz(16 * h + r16);
+            if constexpr (E4M3) {
 #pragma unroll
-            for (int st = 0; st < STEPS; ++st) {
-                x8 kf;
-                if constexpr (E4M3) {
-                    uint32_t u[4];
-                    u[0] = H::from_fp8(t.k[h][st][0], false);
-                    u[1] = H::from_fp8(t.k[h][st][0], true);
-                    u[2] = H::from_fp8(t.k[h][st][1], false);
-                    u[3] = H::from_fp8(t.k[h][st][1], true);
-                    kf = __builtin_bit_cast(x8, *(i32x4_t*)u);
-                } else {
-                    kf = __builtin_bit_cast(x8, *(i32x4_t*)t.k[h][st]);
+                for (int st = 0; st < STEPS; st += 2) {
+                    const i32x4_t w4 = *(const i32x4_t*)(row + ((2 * st + g4) ^ sw) * 16);
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        uint32_t u[4];
+                        u[0] = H::from_fp8(w4[2 * y], false);
+                        u[1] = H::from_fp8(w4[2 * y], true);
+                        u[2] = H::from_fp8(w4[2 * y + 1], false);
+                        u[3] = H::from_fp8(w4[2 * y + 1], true);
+                        s[h] = H::mma(__builtin_bit_cast(x8, *(i32x4_t*)u), qf[st + y], s[h]);
+                    }
                 }
-                s[h] = H::mma(kf, qf[st], s[h]);
+            } else {
+#pragma unroll
+                for (int st = 0; st < STEPS; ++st)
+                    s[h] = H::mma(*(const x8*)(row + ((4 * st + g4) ^ sw) * 16), qf[st], s[h]);
             }
         }
         float x[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = s[j >> 2][j & 3] * p.scale_log2;
         if (!plain) {
+            asm volatile("");  // (a branch: as selects it would run for every tile)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const bool use = usable(vkey(j));
@@ -287,8 +344,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attn_kernel(AttnArgs p
         float top = x[0];
 #pragma unroll
         for (int j = 1; j < 8; ++j) top = fmaxf(top, x[j]);
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
+        top = max_over_groups(top);
         if (__any(top > mx)) {
             const float m2 = fmaxf(mx, top);
             const float f = m2 == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(mx - m2);
@@ -329,33 +385,45 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attn_kernel(AttnArgs p
         }
     };
 
-    // the wave's tiles, 128 keys apart, two register sets in turn
-    int key = start + 32 * wave;
+    // The wave's tiles, a round apart.  While one is computed the next one's keys
+    // and values are on their way (the values' registers in two sets; those of the
+    // keys are free as soon as they are in LDS), and its successor's pages are
+    // looked up (asked for before those loads, so that waiting for them is no wait
+    // for the loads).
+    int key = start + 32 * kw;
     if (key < end) {
-        Tile ta, tb;
-        Where wa = look(key), wb;
-        load(ta, wa);
+        Keys kt;
+        Values va, vb;
+        Where wa = look(key), wb = look(key + round), wc;
+        settle(wa);
+        load_keys(kt, wa);
+        load_values(va, wa);
         for (;;) {
-            const bool more = key + 128 < end;
-            if (more) {
-                wb = look(key + 128);
-                load(tb, wb);
-            }
-            compute(ta, wa, key);
+            settle(wb);
+            wc = look(key + 2 * round);
+            bool more = key + round < end;
+            if (more) load_values(vb, wb);
+            compute(kt, va, wa, key, [&] {
+                if (more) load_keys(kt, wb);
+            });
             if (!more) break;
-            key += 128;
-            const bool again = key + 128 < end;
-            if (again) {
-                wa = look(key + 128);
-                load(ta, wa);
-            }
-            compute(tb, wb, key);
-            if (!again) break;
-            key += 128;
+            key += round;
+            settle(wc);
+            wa = look(key + 2 * round);
+            more = key + round < end;
+            if (more) load_values(va, wc);
+            compute(kt, vb, wb, key, [&] {
+                if (more) load_keys(kt, wc);
+            });
+            if (!more) break;
+            key += round;
+            wb = wa;
+            wa = wc;
         }
     }
 
     // ---- the four waves' parts ------------------------------------------------
+    __syncthreads();  // (the areas of keys end here)
     sum += __shfl_xor(sum, 16);
     sum += __shfl_xor(sum, 32);
     // a NaN among the scores passed by the maximum: as an infinite one it makes
@@ -366,8 +434,13 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attn_kernel(AttnArgs p
         ll_[wave][r16] = sum;
     }
     __syncthreads();
-    const float top = fmaxf(fmaxf(lm_[0][r16], lm_[1][r16]), fmaxf(lm_[2][r16], lm_[3][r16]));
-    const float f = mx == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mx - top);
+    // the largest maximum of the waves that share head hh of the group
+    auto head_top = [&](int hh, int q) {
+        float t = lm_[hh][q];
+        for (int w = hh + p.heads; w < 4; w += p.heads) t = fmaxf(t, lm_[w][q]);
+        return t;
+    };
+    const float f = mx == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mx - head_top(hw, r16));
     // lane l holds elements (4 g + i) VE + m of head l % 16
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -378,21 +451,21 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attn_kernel(AttnArgs p
             *(f32x4_t*)&lo_[wave][r16][(4 * g4 + i) * VE + m] = v;
         }
     __syncthreads();
-    for (int x = threadIdx.x; x < 16 * (DP / 4); x += 256) {
-        const int q = x / (DP / 4), d = (x - q * (DP / 4)) * 4;
+    for (int x = threadIdx.x; x < p.heads * 16 * (DP / 4); x += 256) {
+        const int hh = x / (16 * (DP / 4)), q = x / (DP / 4) % 16, d = x % (DP / 4) * 4;
         if (q >= nh || d >= p.D) continue;
-        const float tq = fmaxf(fmaxf(lm_[0][q], lm_[1][q]), fmaxf(lm_[2][q], lm_[3][q]));
+        const float tq = head_top(hh, q);
         f32x4_t a = {};
         float l = 0.0f;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
+        for (int w = hh; w < 4; w += p.heads) {
             a += *(f32x4_t*)&lo_[w][q][d];
             const float mw = lm_[w][q];
             l += mw == kNegInf ? 0.0f : ll_[w][q] * __builtin_amdgcn_exp2f(mw - tq);
         }
-        const int64_t row = (int64_t)b * p.Hq + h0 + q;
+        const int h = (hk - hw + hh) * p.G + qb * 16 + q;
+        const int64_t row = (int64_t)b * p.Hq + h;
         if (p.splits > 1) {
-            const int64_t at = row * p.splits + blockIdx.x;
+            const int64_t at = row * p.splits + split;
             *(f32x4_t*)(p.po + at * p.D + d) = a;
             if (d == 0) {
                 p.pml[2 * at] = tq;
@@ -400,7 +473,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attn_kernel(AttnArgs p
             }
         } else {
             const float z = tq == kNegInf ? 0.0f : p.v_scale / l;
-            T* out = (T*)p.out.p + b * p.out.ts + (int64_t)(h0 + q) * p.out.hs + d;
+            T* out = (T*)p.out.p + b * p.out.ts + (int64_t)h * p.out.hs + d;
             store4<T>(out, a[0] * z, a[1] * z, a[2] * z, a[3] * z);
             if (d == 0 && p.lse)
                 p.lse[row] = tq == kNegInf ? kNegInf : 0.6931471805599453f * tq + logf(l);
@@ -408,50 +481,57 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attn_kernel(AttnArgs p
     }
 }
 
-// Joins the chunks of one sequence and query head: DL lanes x 4 elements, 256 / DL
-// chunks at a time.
+// Joins the chunks of one sequence and query head: DL lanes x 4 elements (blockIdx.z
+// picks which), 256 / DL chunks at a time, at most kJoinDeep times.  Bound by
+// latency -- the parts come from other XCDs' caches -- so every load of a part is
+// under way before the weights that it waits for are computed.
+constexpr int kJoinDeep = 8;
 template <class T, int DL>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs p) {
     __shared__ float wt[kAttnMaxSplits];
-    __shared__ float red[4];
+    __shared__ float red[2][4];
     __shared__ __attribute__((aligned(16))) float join[256 / DL][DL * 4];
+    constexpr int PARTS = 256 / DL;
     const int h = blockIdx.x, b = blockIdx.y;
     const Range rg = range_of(p, b);
     const int n = (int)(((int64_t)rg.len - rg.base + p.chunk - 1) / p.chunk);
     const int64_t row = (int64_t)b * p.Hq + h;
     const float* ml = p.pml + 2 * row * p.splits;
     const int c = threadIdx.x;
+    const int dl = (c % DL) * 4, d = blockIdx.z * DL * 4 + dl, part = c / DL;
     const float m = c < n ? ml[2 * c] : kNegInf;
+    const float lc = c < n ? ml[2 * c + 1] : 0.0f;
+    f32x4_t v[kJoinDeep];
+#pragma unroll
+    for (int i = 0; i < kJoinDeep; ++i) {
+        const int at = part + i * PARTS;
+        v[i] = at < n && d < p.D ? *(const f32x4_t*)(p.po + (row * p.splits + at) * p.D + d) : (f32x4_t){};
+    }
     float top = m;
 #pragma unroll
     for (int x = 1; x < 64; x *= 2) top = fmaxf(top, __shfl_xor(top, x));
-    if ((c & 63) == 0) red[c >> 6] = top;
+    if ((c & 63) == 0) red[0][c >> 6] = top;
     __syncthreads();
-    top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    __syncthreads();
+    top = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
     const float f = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - top);
-    if (c < kAttnMaxSplits) wt[c] = f;
-    float l = c < n ? f * ml[2 * c + 1] : 0.0f;
-    if (m == kNegInf) l = 0.0f;
+    wt[c] = f;
+    float l = m == kNegInf ? 0.0f : f * lc;
 #pragma unroll
     for (int x = 1; x < 64; x *= 2) l += __shfl_xor(l, x);
-    if ((c & 63) == 0) red[c >> 6] = l;
+    if ((c & 63) == 0) red[1][c >> 6] = l;
     __syncthreads();
-    l = red[0] + red[1] + red[2] + red[3];
-    const int d = (c % DL) * 4, part = c / DL;
+    l = red[1][0] + red[1][1] + red[1][2] + red[1][3];
     f32x4_t a = {};
-    if (d < p.D)
-#pragma unroll 4
-        for (int i = part; i < n; i += 256 / DL) {
-            const float w = wt[i];
-            const f32x4_t v = *(const f32x4_t*)(p.po + (row * p.splits + i) * p.D + d);
-            if (w != 0.0f) a += w * v;
-        }
-    *(f32x4_t*)&join[part][d] = a;
+#pragma unroll
+    for (int i = 0; i < kJoinDeep; ++i) {
+        const int at = part + i * PARTS;
+        if (at < n) a += wt[at] * v[i];
+    }
+    *(f32x4_t*)&join[part][dl] = a;
     __syncthreads();
     if (part == 0 && d < p.D) {
 #pragma unroll
-        for (int i = 1; i < 256 / DL; ++i) a += *(f32x4_t*)&join[i][d];
+        for (int i = 1; i < PARTS; ++i) a += *(f32x4_t*)&join[i][dl];
         const float z = top == kNegInf ? 0.0f : p.v_scale / l;
         T* out = (T*)p.out.p + b * p.out.ts + (int64_t)h * p.out.hs + d;
         store4<T>(out, a[0] * z, a[1] * z, a[2] * z, a[3] * z);
@@ -461,14 +541,19 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs p) {
 
 template <class T, int DP, bool E4M3>
 hipError_t run(const AttnArgs& a, hipStream_t st) {
-    const dim3 grid(a.splits, a.Hk * a.qblocks, a.B);
+    const dim3 grid((uint32_t)a.splits * a.B * (a.Hk / a.heads) * a.qblocks);
     if (a.page_size % 16 == 0)
         hipLaunchKernelGGL((attn_kernel<T, DP, E4M3, true>), grid, dim3(256), 0, st, a);
     else
         hipLaunchKernelGGL((attn_kernel<T, DP, E4M3, false>), grid, dim3(256), 0, st, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits == 1) return e;
-    hipLaunchKernelGGL((attn_join_kernel<T, DP / 4>), dim3(a.Hq, a.B), dim3(256), 0, st, a);
+    // a whole row a workgroup where that takes its chunks in kJoinDeep turns,
+    // else 32 elements
+    if (a.splits <= kJoinDeep * (256 / (DP / 4)))
+        hipLaunchKernelGGL((attn_join_kernel<T, DP / 4>), dim3(a.Hq, a.B), dim3(256), 0, st, a);
+    else
+        hipLaunchKernelGGL((attn_join_kernel<T, 8>), dim3(a.Hq, a.B, DP / 32), dim3(256), 0, st, a);
     return hipGetLastError();
 }
 
