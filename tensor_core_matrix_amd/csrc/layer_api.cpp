@@ -185,16 +185,21 @@ tcm_status check_attn_sizes(int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_
 
 // ---- adapters ------------------------------------------------------------------------
 
-// Parts of K in the adapters' first product: with few rows there are few (block,
-// adapter) pairs, and K is what is left to spread over the compute units; a
-// part is at least 512 values, two steps of each of a workgroup's eight waves.
+// Parts of K in the adapters' first product, such that its workgroups -- one for
+// each row with few rows, for each 16 rows with many -- are about 1024, four for every
+// compute unit, whose reads' latency they hide from each other.  A part is at least
+// 1024 values, a 128-deep piece for each of a workgroup's eight waves, and there are
+// at most four (eight below 16 rows), the reads of t that the second product has
+// under way at once.
 int64_t lora_parts(int64_t M, int64_t K, int64_t* kpart) {
-    int64_t n = M > 0 ? 256 / M : 1;
-    if (n > 8) n = 8;
-    if (n > K / 512) n = K / 512;
+    const int64_t groups = M <= 256 ? M : cdiv(M, 16);
+    int64_t n = groups > 0 ? 1024 / groups : 1;
+    const int64_t most = M < 16 ? 8 : 4;
+    if (n > most) n = most;
+    if (n > K / 1024) n = K / 1024;
     if (n < 1) n = 1;
-    *kpart = cdiv(cdiv(K, n), 256) * 256;
-    if (*kpart < 256) *kpart = 256;
+    *kpart = cdiv(cdiv(K, n), 1024) * 1024;
+    if (*kpart < 1024) *kpart = 1024;
     n = cdiv(K, *kpart);
     return n > 0 ? n : 1;
 }

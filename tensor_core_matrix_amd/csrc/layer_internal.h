@@ -94,7 +94,7 @@ struct LoraArgs {
     int32_t M, N, K, L, R;
     int32_t ldx, ldo;
     int32_t ksplit;  // parts of K in t
-    int32_t kpart;   // K values of one part (a multiple of 32)
+    int32_t kpart;   // K values of one part (a multiple of 1024)
 };
 
 constexpr int kLoraMaxRank = 128;

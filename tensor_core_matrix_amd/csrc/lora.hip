@@ -14,24 +14,47 @@ namespace tcm {
 
 namespace {
 
+// 16 rows x 256 bytes in LDS, row after row; 16 bytes c of a row lie at c ^ row, so
+// that 16 rows' reads of one piece meet 16 groups of banks.
+__device__ __forceinline__ void* piece_at(char* area, int row, int c) {
+    return area + row * 256 + ((c ^ row) * 16);
+}
+
 // ---- t = s_a (X A_a^T) ----------------------------------------------------------
-// A workgroup takes a block of 16 rows, and of the adapters that they name those
-// whose first row in the block is blockIdx.x % slots (+ slots, ...).  Per adapter
-// the 16 rows are multiplied by A_a on the matrix cores, eight waves taking
-// 32-deep steps in turn, and the rows that name it keep the result.  Bound by
-// reading A (each adapter once per block that names it).
+// A workgroup takes a block of 16 rows and a part of K, and of the adapters that the
+// rows name those whose first row in the block is blockIdx.x % slots (+ slots, ...).
+// Per adapter the 16 rows are multiplied by A_a on the matrix cores, eight waves
+// taking 128-deep pieces of K in turn, and the rows that name it keep the result.
+// Bound by reading X and A, which come in whole 256-byte stretches of their rows and
+// are turned into operands through a wave's own LDS areas: rows are often a power
+// of two apart, and the operand's own 16 rows x 64 bytes then meet few channels
+// (4096 rows of 8 KiB: 12 us, and 20 that way).
 template <class T, int RB>
 __global__ __launch_bounds__(512) void lora_shrink_kernel(LoraArgs p, int slots) {
     typedef LoraMma<T> O;
     typedef typename O::x8 x8;
-    __shared__ __attribute__((aligned(16))) float red[8][16][RB * 16 + 4];
+    constexpr int RED = 8 * 16 * (RB * 16 + 4) * 4, AREAS = 8 * 2 * 4096;
+    __shared__ __attribute__((aligned(1024))) char lds[RED > AREAS ? RED : AREAS];
+    float(*const red)[16][RB * 16 + 4] = (float(*)[16][RB * 16 + 4])lds;
     const int lane = threadIdx.x & 63, r16 = lane & 15, g4 = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int m0 = (int)(blockIdx.x / slots) * 16, s0 = blockIdx.x % slots;
     const int k0 = blockIdx.y * p.kpart, k1 = min(p.K, k0 + p.kpart);
     const int id = lora_row(p, m0, r16);
     uint32_t left = (uint32_t)__ballot(id >= 0) & 0xffffu;
-    const T* xr = (const T*)p.X + (int64_t)min(m0 + r16, p.M - 1) * p.ldx + 8 * g4;
+    char* const xa = lds + wave * 8192;
+    char* const aa = xa + 4096;
+    // lane: row 4 x + lane / 16 of 16, 16 bytes lane % 16
+    auto load = [&](i32x4_t (&v)[4], const T* base, int rows, int64_t ld, int k) {
+        const bool in = k + 8 * r16 < k1;
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            v[x] = in ? *(const i32x4_t*)(base + min(4 * x + g4, rows - 1) * ld + k + 8 * r16) : (i32x4_t){};
+    };
+    auto store = [&](char* area, const i32x4_t (&v)[4]) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) *(i32x4_t*)piece_at(area, 4 * x + g4, r16) = v[x];
+    };
     while (left) {
         const int first = __builtin_ctz(left);
         const int a = __builtin_amdgcn_readlane(id, first);
@@ -39,35 +62,38 @@ __global__ __launch_bounds__(512) void lora_shrink_kernel(LoraArgs p, int slots)
         left &= ~rows;
         if (first % slots != s0) continue;
         const int rank = lora_rank(p, a);
+        const T* const xb = (const T*)p.X + (int64_t)m0 * p.ldx;
+        const T* const ab = (const T*)p.A + (int64_t)a * p.R * p.K;
         f32x4_t acc[RB];
 #pragma unroll
         for (int i = 0; i < RB; ++i) acc[i] = (f32x4_t){};
-        const T* ar[RB];
+        constexpr int AN = RB < 2 ? RB : 2;  // blocks of 16 ranks read at once
+        for (int k = k0 + 128 * wave; k < k1; k += 1024) {
+            i32x4_t xv[4];
+            load(xv, xb, min(16, p.M - m0), p.ldx, k);
 #pragma unroll
-        for (int i = 0; i < RB; ++i)
-            ar[i] = (const T*)p.A + ((int64_t)a * p.R + min(16 * i + r16, p.R - 1)) * p.K + 8 * g4;
-        constexpr int U = RB <= 2 ? 4 : 2;
-        int k = k0 + 32 * wave;
-        for (; k + 256 * (U - 1) + 32 <= k1; k += 256 * U) {
-            x8 x[U], f[U][RB];
+            for (int i0 = 0; i0 < RB; i0 += AN) {
+                i32x4_t av[AN][4];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                x[u] = *(const x8*)(xr + k + 256 * u);
+                for (int i = 0; i < AN; ++i)
+                    if (16 * (i0 + i) < p.R)
+                        load(av[i], ab + (int64_t)16 * (i0 + i) * p.K, min(16, p.R - 16 * (i0 + i)), p.K, k);
+                wave_lds_exchange();
+                if (i0 == 0) store(xa, xv);
 #pragma unroll
-                for (int i = 0; i < RB; ++i) f[u][i] = *(const x8*)(ar[i] + k + 256 * u);
+                for (int i = 0; i < AN; ++i) {
+                    if (16 * (i0 + i) >= p.R) continue;
+                    store(aa, av[i]);
+                    wave_lds_exchange();
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        acc[i0 + i] = O::mma(*(const x8*)piece_at(aa, r16, 4 * s + g4),
+                                             *(const x8*)piece_at(xa, r16, 4 * s + g4), acc[i0 + i]);
+                    wave_lds_exchange();
+                }
             }
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int i = 0; i < RB; ++i) acc[i] = O::mma(f[u][i], x[u], acc[i]);
         }
-        for (; k < k1; k += 256) {  // (the last step may be cut by K)
-            const bool in = k + 8 * g4 < k1;
-            const x8 x = in ? *(const x8*)(xr + k) : (x8){};
-#pragma unroll
-            for (int i = 0; i < RB; ++i)
-                acc[i] = O::mma(in ? *(const x8*)(ar[i] + k) : (x8){}, x, acc[i]);
-        }
+        __syncthreads();  // (the areas end here)
 #pragma unroll
         for (int i = 0; i < RB; ++i) *(f32x4_t*)&red[wave][r16][16 * i + 4 * g4] = acc[i];
         __syncthreads();
@@ -84,96 +110,196 @@ __global__ __launch_bounds__(512) void lora_shrink_kernel(LoraArgs p, int slots)
     }
 }
 
+constexpr int kNonTemporal = 2;  // cache policy of a buffer load: read once
+
 // ---- few rows ---------------------------------------------------------------------
 // Bound by reading W once.  A workgroup owns 16 NB output columns for all 16 MB >= M
-// rows; its eight waves take the 32-deep K steps in turn, reading W from memory
-// straight into operand registers (no element of W is used twice), and their
-// sums meet in LDS.  The adapters are dealt to the waves too: what an adapter adds
-// to a block of rows is one more term of that sum.
+// rows.  WW of its sixteen waves take W, pieces of K in turn: whole stretches of its
+// rows (a probe reads 6.4 TB/s that way, and 5.2 in the operand's own pattern of 16
+// rows x 64 bytes), which a wave turns into operands through its own LDS area, the
+// next piece on its way while one is multiplied.  The other waves take what the
+// adapters add, a row a wave in turn: with few rows nearly every row has an
+// adapter of its own, so there is nothing for the matrix cores to share, and a
+// row's 16 NB dot products over the ranks are done by its lanes, in fp32 and from
+// nothing but the row's own adapter.  Everything meets in LDS at the end.
 template <class T, class TO, int MB, int NB>
-__global__ __launch_bounds__(512) void lora_rows_kernel(LoraArgs p) {
+__global__ __launch_bounds__(1024) void lora_rows_kernel(LoraArgs p) {
     typedef LoraMma<T> O;
     typedef typename O::x8 x8;
-    __shared__ __attribute__((aligned(16))) f32x4_t red[8][MB * NB][64];
+    constexpr int WW = 8, LW = 16 - WW;        // waves that take W, and adapters
+    constexpr int PB = 256 / NB;               // bytes of a row's piece,
+    constexpr int PK = PB / 2, S = PK / 32;    // its K values and 32-deep steps
+    constexpr int LR = PB / 16, RN = 64 / LR;  // lanes that read it, rows of one read
+    constexpr int AREA = 4096;
+    __shared__ __attribute__((aligned(1024))) char areas[WW * AREA];
+    __shared__ __attribute__((aligned(1024))) f32x4_t red[WW + 1][MB * NB][64];
+    __shared__ __attribute__((aligned(16))) float ts[LW][4][kLoraMaxRank];
     const int lane = threadIdx.x & 63, r16 = lane & 15, g4 = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n0 = blockIdx.x * 16 * NB;
-    f32x4_t acc[MB][NB];
+    if (wave < WW) {
+        f32x4_t acc[MB][NB];
 #pragma unroll
-    for (int i = 0; i < MB; ++i)
+        for (int i = 0; i < MB; ++i)
 #pragma unroll
-        for (int j = 0; j < NB; ++j) acc[i][j] = (f32x4_t){};
-    const T* wr[NB];
-    const T* xr[MB];
+            for (int j = 0; j < NB; ++j) acc[i][j] = (f32x4_t){};
+        // lane: row RN x + lane / LR of the columns' rows, 16 bytes lane % LR; past the
+        // last row or K the buffers give zeros
+        const int wc = lane % LR, wr = lane / LR;
+        const uint32_t wrow = (uint32_t)p.K * 2u, xrow = (uint32_t)p.ldx * 2u;
+        const __amdgpu_buffer_rsrc_t rw = make_rsrc((const T*)p.W + (int64_t)n0 * p.K,
+                                                    (uint32_t)min(16 * NB, p.N - n0) * wrow);
+        const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.X, (uint32_t)(p.M - 1) * xrow + wrow);
+        const uint32_t w0 = (uint32_t)wr * wrow + 16u * wc, x0 = (uint32_t)r16 * xrow + 16u * g4;
+        char* const area = areas + wave * AREA;
+        // 16 bytes c of a row lie at c ^ swz(row): 16 rows' reads meet 16 bank groups
+        auto swz = [](int row) { return LR == 16 ? row & 15 : (row >> 1) & 7; };
+        auto load = [&](i32x4_t (&w)[4], int k) {
+            const uint32_t at = k + 8 * wc < p.K ? w0 + 2u * (uint32_t)k : kOutOfRange;
 #pragma unroll
-    for (int j = 0; j < NB; ++j)
-        wr[j] = (const T*)p.W + (int64_t)min(n0 + 16 * j + r16, p.N - 1) * p.K + 8 * g4;
+            for (int x = 0; x < 4; ++x)
+                w[x] = __builtin_bit_cast(i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                                       rw, at + (uint32_t)(RN * x) * wrow, 0, kNonTemporal));
+        };
+        // X comes from the caches, its reads ahead of the next piece's of W: a wave's
+        // loads return in order, and W's would be waited for with them
+        x8 xf[S][MB];
+        auto load_x = [&](int k) {
 #pragma unroll
-    for (int i = 0; i < MB; ++i)
-        xr[i] = (const T*)p.X + (int64_t)min(16 * i + r16, p.M - 1) * p.ldx + 8 * g4;
-    constexpr int U = 8 / NB;
-    int k = 32 * wave;
-    for (; k + 256 * (U - 1) + 32 <= p.K; k += 256 * U) {
-        x8 w[U][NB];
+            for (int s = 0; s < S; ++s) {
+                const uint32_t at = k + 32 * s + 8 * g4 < p.K ? x0 + 2u * (uint32_t)(k + 32 * s) : kOutOfRange;
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int j = 0; j < NB; ++j) w[u][j] = *(const x8*)(wr[j] + k + 256 * u);
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int i = 0; i < MB; ++i) {
-                const x8 x = *(const x8*)(xr[i] + k + 256 * u);
-#pragma unroll
-                for (int j = 0; j < NB; ++j) acc[i][j] = O::mma(w[u][j], x, acc[i][j]);
+                for (int i = 0; i < MB; ++i) {
+                    // (a row past M may lie before the buffer's end)
+                    const uint32_t row = 16 * i + r16 < p.M ? at + (uint32_t)(16 * i) * xrow : kOutOfRange;
+                    xf[s][i] = __builtin_bit_cast(x8, __builtin_amdgcn_raw_buffer_load_b128(rx, row, 0, 0));
+                }
             }
-    }
-    for (; k < p.K; k += 256) {
-        const bool in = k + 8 * g4 < p.K;
-        x8 w[NB];
+        };
+        auto multiply = [&](const i32x4_t (&w)[4]) {
+            wave_lds_exchange();
 #pragma unroll
-        for (int j = 0; j < NB; ++j) w[j] = in ? *(const x8*)(wr[j] + k) : (x8){};
+            for (int x = 0; x < 4; ++x) {
+                const int row = RN * x + wr;
+                *(i32x4_t*)(area + row * PB + ((wc ^ swz(row)) * 16)) = w[x];
+            }
+            wave_lds_exchange();
 #pragma unroll
-        for (int i = 0; i < MB; ++i) {
-            const x8 x = in ? *(const x8*)(xr[i] + k) : (x8){};
+            for (int s = 0; s < S; ++s)
 #pragma unroll
-            for (int j = 0; j < NB; ++j) acc[i][j] = O::mma(w[j], x, acc[i][j]);
+                for (int j = 0; j < NB; ++j) {
+                    const x8 f = *(const x8*)(area + (16 * j + r16) * PB + (((4 * s + g4) ^ swz(r16)) * 16));
+#pragma unroll
+                    for (int i = 0; i < MB; ++i) acc[i][j] = O::mma(f, xf[s][i], acc[i][j]);
+                }
+        };
+        i32x4_t wa[4], wb[4];
+        int k = PK * wave;
+        constexpr int STEP = PK * WW;
+        if (k < p.K) load(wa, k);
+        while (k < p.K) {
+            load_x(k);
+            if (k + STEP < p.K) load(wb, k + STEP);
+            multiply(wa);
+            k += STEP;
+            if (k >= p.K) break;
+            load_x(k);
+            if (k + STEP < p.K) load(wa, k + STEP);
+            multiply(wb);
+            k += STEP;
+        }
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+#pragma unroll
+            for (int j = 0; j < NB; ++j) red[wave][i * NB + j][lane] = acc[i][j];
+    } else {
+        // lane: column lane % C and the ranks 8 (lane / C), + 8 P, .. of it
+        constexpr int C = 16 * NB, P = 64 / C;
+        const int lw = wave - WW, c = lane % C, part = lane / C;
+        const int n = min(n0 + c, p.N - 1);
+        // row m's sum for column c in the layout of the products' sums
+        auto put = [&](int m, float v) {
+            float* at = (float*)&red[WW][(m >> 4) * NB + (c >> 4)][(m & 15) + 16 * ((c & 15) >> 2)];
+            if (part == 0) at[c & 3] = v;
+        };
+        const int id = lora_row(p, 0, lane);  // of row `lane`
+        // four rows at a time, all their reads under way together: the first BN
+        // pieces of B_a's row, and t (the parts of K summed, lane r rank r), which
+        // goes through LDS (the wave's own: its operations run in order)
+        constexpr int BN = 2, QN = 4;
+        for (int m0 = lw; m0 < 16 * MB; m0 += QN * LW) {
+            int a[QN], rank[QN];
+            x8 b[QN][BN];
+            float t[QN][kLoraMaxRank / 64];
+            const T* br[QN];
+#pragma unroll
+            for (int q = 0; q < QN; ++q) {
+                const int m = m0 + q * LW;
+                a[q] = m < 16 * MB ? __builtin_amdgcn_readlane(id, m & 63) : -1;
+                rank[q] = a[q] >= 0 ? lora_rank(p, a[q]) : 0;
+            }
+#pragma unroll
+            for (int q = 0; q < QN; ++q) {
+                br[q] = (const T*)p.B + ((int64_t)max(a[q], 0) * p.N + n) * p.R + 8 * part;
+#pragma unroll
+                for (int i = 0; i < BN; ++i)
+                    b[q][i] = 8 * (part + P * i) < rank[q] ? *(const x8*)(br[q] + 8 * P * i) : (x8){};
+            }
+#pragma unroll
+            for (int q = 0; q < QN; ++q)
+#pragma unroll
+                for (int h = 0; h < kLoraMaxRank / 64; ++h) {
+                    const int r = lane + 64 * h;
+                    float v = 0.0f;
+                    if (r < rank[q]) {
+                        const float* tr = p.t + (int64_t)(m0 + q * LW) * p.R + r;
+                        for (int s = 0; s < p.ksplit; s += 4) {
+                            float u[4];
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                u[x] = tr[(int64_t)min(s + x, p.ksplit - 1) * p.M * p.R];
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) v += s + x < p.ksplit ? u[x] : 0.0f;
+                        }
+                    }
+                    t[q][h] = v;
+                }
+            wave_lds_exchange();
+#pragma unroll
+            for (int q = 0; q < QN; ++q)
+#pragma unroll
+                for (int h = 0; h < kLoraMaxRank / 64; ++h) ts[lw][q][lane + 64 * h] = t[q][h];
+            wave_lds_exchange();
+#pragma unroll
+            for (int q = 0; q < QN; ++q) {
+                float sum = 0.0f;
+                for (int i0 = 0; 8 * P * i0 < rank[q]; i0 += BN) {
+                    if (i0 > 0)
+#pragma unroll
+                        for (int i = 0; i < BN; ++i)
+                            b[q][i] = 8 * (part + P * (i0 + i)) < rank[q] ? *(const x8*)(br[q] + 8 * P * (i0 + i))
+                                                                          : (x8){};
+#pragma unroll
+                    for (int i = 0; i < BN; ++i) {
+                        const int r = 8 * (part + P * (i0 + i));
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            sum += r + e < rank[q] ? ts[lw][q][r + e] * (float)b[q][i][e] : 0.0f;
+                    }
+                }
+#pragma unroll
+                for (int x = C; x < 64; x *= 2) sum += __shfl_xor(sum, x);
+                if (m0 + q * LW < 16 * MB) put(m0 + q * LW, sum);
+            }
+            wave_lds_exchange();
         }
     }
-    int turn = 0;
-#pragma unroll
-    for (int i = 0; i < MB; ++i) {
-        const int id = lora_row(p, 16 * i, r16);
-        uint32_t left = (uint32_t)__ballot(id >= 0) & 0xffffu;
-        while (left) {
-            const int a = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
-            left &= ~(uint32_t)__ballot(id == a);
-            if ((turn++ & 7) != wave) continue;
-            const int rank = lora_rank(p, a);
-            f32x4_t d[NB];
-#pragma unroll
-            for (int j = 0; j < NB; ++j) d[j] = (f32x4_t){};
-            for (int r0 = 0; r0 < rank; r0 += 16) {
-                const x8 t = lora_t<T>(p, 16 * i + r16, r0, g4, id == a);
-#pragma unroll
-                for (int j = 0; j < NB; ++j)
-                    d[j] = O::mma(lora_b<T>(p, a, rank, n0 + 16 * j + r16, r0, g4), t, d[j]);
-            }
-            if (id == a)
-#pragma unroll
-                for (int j = 0; j < NB; ++j) acc[i][j] += d[j];
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < MB; ++i)
-#pragma unroll
-        for (int j = 0; j < NB; ++j) red[wave][i * NB + j][lane] = acc[i][j];
     __syncthreads();
-    for (int x = threadIdx.x; x < MB * NB * 64; x += 512) {
+    for (int x = threadIdx.x; x < MB * NB * 64; x += 1024) {
         const int blk = x >> 6, l = x & 63;
         f32x4_t s = red[0][blk][l];
 #pragma unroll
-        for (int w = 1; w < 8; ++w) s += red[w][blk][l];
+        for (int w = 1; w < WW + 1; ++w) s += red[w][blk][l];
         const int m = 16 * (blk / NB) + (l & 15), n = n0 + 16 * (blk % NB) + 4 * (l >> 4);
         if (m >= p.M) continue;
         TO* row = (TO*)p.out + (int64_t)m * p.ldo;
@@ -188,19 +314,21 @@ __global__ __launch_bounds__(512) void lora_rows_kernel(LoraArgs p) {
 }
 
 // ---- many rows ----------------------------------------------------------------------
-// BM x BN tiles, four waves in a 2 x 2 arrangement, 64-deep slices by DMA into a ring
-// of S stages (128-byte rows whose 16-byte chunk c lies at c ^ (row / 2) % 8, so that
-// 16 rows' reads meet 16 bank groups), one barrier a slice.
-template <class T, class TO, int BM, int BN, int S>
-__global__ __launch_bounds__(256) void lora_tile_kernel(LoraArgs p, int tiles_m, int tiles_n) {
+// BM x BN tiles, WM x WN waves, 64-deep slices by DMA into a ring of S stages (128-byte
+// rows whose 16-byte chunk c lies at c ^ (row / 2) % 8, so that 16 rows' reads meet 16
+// bank groups), one barrier a slice.
+template <class T, class TO, int BM, int BN, int S, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN, 2) void lora_tile_kernel(LoraArgs p, int tiles_m, int tiles_n) {
     typedef LoraMma<T> O;
     typedef typename O::x8 x8;
-    constexpr int STAGE = (BM + BN) * 128, CA = BM / 32, CB = BN / 32, C = CA + CB;
-    constexpr int FM = BM / 32, FN = BN / 32;
+    constexpr int WV = WM * WN, ROWS = 8 * WV;  // rows of one copy by all waves
+    constexpr int STAGE = (BM + BN) * 128, CA = BM / ROWS, CB = BN / ROWS, C = CA + CB;
+    constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
+    static_assert((ROWS / 2) % 8 == 0 || ROWS % 16 == 0, "a lane's chunk is the same in every copy");
     __shared__ __attribute__((aligned(1024))) char lds[S * STAGE];
     const int lane = threadIdx.x & 63, r16 = lane & 15, g4 = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = wave >> 1, wn = wave & 1;
+    const int wm = wave / WN, wn = wave % WN;
     // tiles down groups of 4 tile rows, neighbours on one XCD
     GemmArgs order;
     order.tiles_m = tiles_m;
@@ -226,12 +354,13 @@ __global__ __launch_bounds__(256) void lora_tile_kernel(LoraArgs p, int tiles_m,
         for (int x = 0; x < CA; ++x)
             // (rows past the tile's last are past the buffer's end, or hold K
             // values of the next row that no output uses)
-            copy16_to_lds(ra, dst + x * 4096,
-                          in && 32 * x + cp_row < rows_a ? (uint32_t)(32 * x + cp_row) * lda + at : kOutOfRange);
+            copy16_to_lds(ra, dst + x * ROWS * 128,
+                          in && ROWS * x + cp_row < rows_a ? (uint32_t)(ROWS * x + cp_row) * lda + at
+                                                           : kOutOfRange);
 #pragma unroll
         for (int x = 0; x < CB; ++x)
-            copy16_to_lds(rb, dst + (CA + x) * 4096,
-                          in ? (uint32_t)(32 * x + cp_row) * ldb + at : kOutOfRange);
+            copy16_to_lds(rb, dst + (CA + x) * ROWS * 128,
+                          in ? (uint32_t)(ROWS * x + cp_row) * ldb + at : kOutOfRange);
     };
     f32x4_t acc[FM][FN];
 #pragma unroll
@@ -252,10 +381,10 @@ __global__ __launch_bounds__(256) void lora_tile_kernel(LoraArgs p, int tiles_m,
             x8 fa[FM], fb[FN];
 #pragma unroll
             for (int i = 0; i < FM; ++i)
-                fa[i] = *(const x8*)(st + (wm * (BM / 2) + 16 * i + r16) * 128 + ch);
+                fa[i] = *(const x8*)(st + (wm * (BM / WM) + 16 * i + r16) * 128 + ch);
 #pragma unroll
             for (int j = 0; j < FN; ++j)
-                fb[j] = *(const x8*)(st + (BM + wn * (BN / 2) + 16 * j + r16) * 128 + ch);
+                fb[j] = *(const x8*)(st + (BM + wn * (BN / WN) + 16 * j + r16) * 128 + ch);
 #pragma unroll
             for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -263,29 +392,12 @@ __global__ __launch_bounds__(256) void lora_tile_kernel(LoraArgs p, int tiles_m,
         }
     }
     wait_vmcnt<0>();  // (copies of slices past the last: zeros, but still on their way)
-    const int m0 = tm * BM + wm * (BM / 2), n0 = tn * BN + wn * (BN / 2);
-#pragma unroll
-    for (int i = 0; i < FM; ++i) {
-        const int id = lora_row(p, m0 + 16 * i, r16);
-        uint32_t left = (uint32_t)__ballot(id >= 0) & 0xffffu;
-        while (left) {
-            const int a = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
-            left &= ~(uint32_t)__ballot(id == a);
-            const int rank = lora_rank(p, a);
-            f32x4_t d[FN];
-#pragma unroll
-            for (int j = 0; j < FN; ++j) d[j] = (f32x4_t){};
-            for (int r0 = 0; r0 < rank; r0 += 16) {
-                const x8 t = lora_t<T>(p, m0 + 16 * i + r16, r0, g4, id == a);
-#pragma unroll
-                for (int j = 0; j < FN; ++j)
-                    d[j] = O::mma(lora_b<T>(p, a, rank, n0 + 16 * j + r16, r0, g4), t, d[j]);
-            }
-            if (id == a)
-#pragma unroll
-                for (int j = 0; j < FN; ++j) acc[i][j] += d[j];
-        }
-    }
+    const int m0 = tm * BM + wm * (BM / WM), n0 = tn * BN + wn * (BN / WN);
+    constexpr bool FULL = sizeof(TO) == 4 && std::is_same<T, __bf16>::value;
+    if constexpr (FM * FN >= 32)
+        lora_add_lean<T, FULL>(p, acc, m0, n0);
+    else
+        lora_add<T, FULL>(p, acc, m0, n0);
     const bool vec = (p.ldo & 3) == 0;
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
@@ -317,24 +429,51 @@ void shrink(const LoraArgs& a, hipStream_t st) {
                        st, a, slots);
 }
 
-template <class T, class TO, int BM, int BN, int S>
+template <class T, class TO, int BM, int BN, int S, int WM, int WN>
 void tiles(const LoraArgs& a, hipStream_t st) {
     const int tm = cdiv_i(a.M, BM), tn = cdiv_i(a.N, BN);
-    hipLaunchKernelGGL((lora_tile_kernel<T, TO, BM, BN, S>), dim3(tm * tn), dim3(256), 0, st, a, tm, tn);
+    hipLaunchKernelGGL((lora_tile_kernel<T, TO, BM, BN, S, WM, WN>), dim3(tm * tn), dim3(64 * WM * WN), 0,
+                       st, a, tm, tn);
+}
+
+template <class T, class TO, int MB, int NB>
+void rows(const LoraArgs& a, hipStream_t st) {
+    hipLaunchKernelGGL((lora_rows_kernel<T, TO, MB, NB>), dim3(cdiv_i(a.N, 16 * NB)), dim3(1024), 0, st, a);
 }
 
 template <class T, class TO>
 void product(const LoraArgs& a, int cus, hipStream_t st) {
-    if (a.M <= 16)
-        hipLaunchKernelGGL((lora_rows_kernel<T, TO, 1, 1>), dim3(cdiv_i(a.N, 16)), dim3(512), 0, st, a);
-    else if (a.M <= 32)
-        hipLaunchKernelGGL((lora_rows_kernel<T, TO, 2, 1>), dim3(cdiv_i(a.N, 16)), dim3(512), 0, st, a);
-    else if (a.M <= 64)
-        hipLaunchKernelGGL((lora_rows_kernel<T, TO, 4, 2>), dim3(cdiv_i(a.N, 32)), dim3(512), 0, st, a);
-    else if ((int64_t)cdiv_i(a.M, 128) * cdiv_i(a.N, 128) >= cus)
-        tiles<T, TO, 128, 128, 2>(a, st);
+    // Few rows.  32 columns a workgroup read X half as often as 16, which counts from
+    // two blocks of rows on, where they still give every compute unit a workgroup
+    // (N = 8192: 48 rows 37 us, and 51 with 16; one row 21, and 16 with 16;
+    // N = 4096, 48 rows: 33, and 30 with 16).
+    const int mb = cdiv_i(a.M, 16);
+    const bool wide = mb > 1 && cdiv_i(a.N, 32) >= cus;
+    if (mb <= 4) {
+        switch (2 * mb + wide) {
+        case 2: rows<T, TO, 1, 1>(a, st); break;
+        case 4: rows<T, TO, 2, 1>(a, st); break;
+        case 5: rows<T, TO, 2, 2>(a, st); break;
+        case 6: rows<T, TO, 3, 1>(a, st); break;
+        case 7: rows<T, TO, 3, 2>(a, st); break;
+        case 8: rows<T, TO, 4, 1>(a, st); break;
+        case 9: rows<T, TO, 4, 2>(a, st); break;
+        }
+    }
+    if (mb <= 4) return;
+    // The largest tile that still gives every compute unit one (128 x 64: three in
+    // four of them).  4096^3: 256 x 256 129 us, 128 x 128 134, 128 x 64 165; 2048 rows
+    // of 4096 x 4096: 112, 71 and 87; 333 rows: 128 x 64 27, 64 x 64 28; 128 rows: 25
+    // and 21.
+    auto count = [&](int64_t bm, int64_t bn) { return (int64_t)cdiv_i(a.M, bm) * cdiv_i(a.N, bn); };
+    if (count(256, 256) >= cus)
+        tiles<T, TO, 256, 256, 2, 4, 2>(a, st);
+    else if (count(128, 128) >= cus)
+        tiles<T, TO, 128, 128, 2, 2, 2>(a, st);
+    else if (4 * count(128, 64) >= 3 * cus)
+        tiles<T, TO, 128, 64, 3, 4, 2>(a, st);
     else
-        tiles<T, TO, 64, 64, 4>(a, st);
+        tiles<T, TO, 64, 64, 4, 2, 2>(a, st);
 }
 
 template <class T>

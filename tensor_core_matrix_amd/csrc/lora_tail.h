@@ -8,7 +8,8 @@
 // positions 0..15 and what they leave in 16..31, against the same 16 columns
 // of B_a.  (One rounded t would add an error of the size of the output's own
 // rounding where the adapter is as large as the projection; the second half
-// costs nothing below rank 32 and little above it.)
+// costs nothing below rank 32 and little above it.)  For fp32 outputs of bf16
+// operands a second product adds what the two halves leave.
 //
 // A block is multiplied once for every adapter that its 16 rows name, and only
 // the rows that name it take the result: a row never sees another adapter's
@@ -46,30 +47,52 @@ __device__ __forceinline__ int lora_rank(const LoraArgs& p, int a) {
     return min(max(r, 0), p.R);
 }
 
+// t of row m, ranks r .. r + 7: the parts of K summed, four reads of them under way
+// at a time
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+__device__ __forceinline__ f32x8 lora_t8(const LoraArgs& p, int m, int r) {
+    const float* t = p.t + (int64_t)m * p.R + r;
+    f32x4_t a = {}, b = {};
+    for (int s = 0; s < p.ksplit; s += 4) {
+        f32x4_t u[4], v[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            if (x == 0 || s + x < p.ksplit) {
+                const float* ts = t + (int64_t)(s + x) * p.M * p.R;
+                u[x] = *(const f32x4_t*)ts;
+                v[x] = *(const f32x4_t*)(ts + 4);
+            } else {
+                u[x] = v[x] = (f32x4_t){};
+            }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) a += u[x], b += v[x];
+    }
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
 // The t operand of ranks r0 .. r0 + 15 of the block's rows: lane l holds row
 // l % 16, ranks r0 + 8 (g % 2) + 0..7 of the upper (g < 2) or lower half, g = l / 16.
-// Lanes whose row is not `mine` get zeros (their t was never written).
-template <class T>
+// Lanes whose row is not `mine` get zeros (their t was never written).  REST: what
+// the two halves leave, and zeros beside it.
+template <class T, bool REST = false>
 __device__ __forceinline__ typename LoraMma<T>::x8 lora_t(const LoraArgs& p, int m, int r0, int g4,
                                                           bool mine) {
     typedef typename LoraMma<T>::x8 x8;
     const int r = r0 + 8 * (g4 & 1);
     x8 f = {};
     if (mine && r < p.R) {
-        const float* t = p.t + (int64_t)m * p.R + r;
-        f32x4_t a = *(const f32x4_t*)t, b = *(const f32x4_t*)(t + 4);
-        for (int s = 1; s < p.ksplit; ++s) {
-            const float* ts = t + (int64_t)s * p.M * p.R;
-            a += *(const f32x4_t*)ts;
-            b += *(const f32x4_t*)(ts + 4);
-        }
+        const f32x8 t = lora_t8(p, m, r);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float v = j < 4 ? a[j & 3] : b[j & 3];
-            const T hi = convert_out<T>(v);
-            const float rest = v - (float)hi;
+            const T hi = convert_out<T>(t[j]);
+            const float rest = t[j] - (float)hi;
             // (where the upper half is infinite or NaN it says all)
-            f[j] = g4 < 2 ? hi : rest == rest ? convert_out<T>(rest) : (T)0.0f;
+            const T lo = rest == rest ? convert_out<T>(rest) : (T)0.0f;
+            const float last = rest - (float)lo;
+            if constexpr (REST)
+                f[j] = g4 < 2 && last == last ? convert_out<T>(last) : (T)0.0f;
+            else
+                f[j] = g4 < 2 ? hi : lo;
         }
     }
     return f;
@@ -90,6 +113,146 @@ __device__ __forceinline__ typename LoraMma<T>::x8 lora_b(const LoraArgs& p, int
         }
     }
     return f;
+}
+
+// The adapters' part of a block of 16 NI rows from m0 and 16 NJ columns from n0,
+// added to acc[i][j] (lane l: row 16 i + l % 16, columns 16 j + 4 (l / 16) ..), block of
+// rows by block.  A block that names one or two adapters (the rule where requests
+// bring whole prompts) takes the matrix cores, once for each; one that names more
+// (a decode batch: nearly every row its own) is left to its lanes, each of which
+// adds up its own columns of its own row's adapter in fp32, all of a block's reads
+// under way together: adapter by adapter, 128 rows with 64 adapters (4096 x 4096,
+// rank 16) take 71 us, this way 33.
+template <class T, bool FULL, int NI, int NJ>
+__device__ __forceinline__ void lora_add(const LoraArgs& p, f32x4_t (&acc)[NI][NJ], int m0, int n0) {
+    typedef LoraMma<T> O;
+    typedef typename O::x8 x8;
+    const int lane = threadIdx.x & 63, r16 = lane & 15, g4 = lane >> 4;
+    int ids[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) ids[i] = lora_row(p, m0 + 16 * i, r16);
+    // the wave's whole stretch of rows has one adapter: its operands are read once
+    const int one = __builtin_amdgcn_readfirstlane(ids[0]);
+    bool same = one >= 0;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) same = same && ids[i] == one;
+    if (__ballot(!same) == 0) {
+        const int rank = lora_rank(p, one);
+        for (int r0 = 0; r0 < rank; r0 += 16) {
+            x8 b[NJ], t[NI];
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) b[j] = lora_b<T>(p, one, rank, n0 + 16 * j + r16, r0, g4);
+#pragma unroll
+            for (int i = 0; i < NI; ++i) t[i] = lora_t<T>(p, m0 + 16 * i + r16, r0, g4, true);
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) acc[i][j] = O::mma(b[j], t[i], acc[i][j]);
+            if constexpr (FULL)
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    const x8 u = lora_t<T, true>(p, m0 + 16 * i + r16, r0, g4, true);
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j) acc[i][j] = O::mma(b[j], u, acc[i][j]);
+                }
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        const int m = m0 + 16 * i + r16, id = ids[i];
+        uint32_t left = (uint32_t)__ballot(id >= 0) & 0xffffu;
+        if (!left) continue;
+        const int first = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
+        const uint32_t others = left & ~(uint32_t)__ballot(id == first);
+        const int second = others ? __builtin_amdgcn_readlane(id, __builtin_ctz(others)) : first;
+        if ((others & ~(uint32_t)__ballot(id == second)) == 0) {
+            while (left) {
+                const int a = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
+                left &= ~(uint32_t)__ballot(id == a);
+                const int rank = lora_rank(p, a);
+                f32x4_t d[NJ];
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) d[j] = (f32x4_t){};
+                for (int r0 = 0; r0 < rank; r0 += 16) {
+                    x8 b[NJ];
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j) b[j] = lora_b<T>(p, a, rank, n0 + 16 * j + r16, r0, g4);
+                    const x8 t = lora_t<T>(p, m, r0, g4, id == a);
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j) d[j] = O::mma(b[j], t, d[j]);
+                    if constexpr (FULL) {
+                        const x8 u = lora_t<T, true>(p, m, r0, g4, id == a);
+#pragma unroll
+                        for (int j = 0; j < NJ; ++j) d[j] = O::mma(b[j], u, d[j]);
+                    }
+                }
+                if (id == a)
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j) acc[i][j] += d[j];
+            }
+            continue;
+        }
+        const int rank = id >= 0 ? lora_rank(p, id) : 0;
+        const T* const brow = (const T*)p.B + (int64_t)max(id, 0) * p.N * p.R;
+        for (int r = 0; r < p.R; r += 8) {
+            if (__ballot(r < rank) == 0) break;
+            if (r >= rank) continue;
+            const f32x8 t = lora_t8(p, m, r);
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                x8 b[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    b[e] = *(const x8*)(brow + (int64_t)min(n0 + 16 * j + 4 * g4 + e, p.N - 1) * p.R + r);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float s = 0.0f;
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) s += r + x < rank ? t[x] * (float)b[e][x] : 0.0f;
+                    acc[i][j][e] += s;
+                }
+            }
+        }
+    }
+}
+
+// The same for accumulators that leave few registers: always the matrix cores, block
+// of rows by block and adapter by adapter, four columns' blocks at a time.
+template <class T, bool FULL, int NI, int NJ>
+__device__ __forceinline__ void lora_add_lean(const LoraArgs& p, f32x4_t (&acc)[NI][NJ], int m0, int n0) {
+    typedef LoraMma<T> O;
+    typedef typename O::x8 x8;
+    const int lane = threadIdx.x & 63, r16 = lane & 15, g4 = lane >> 4;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        const int id = lora_row(p, m0 + 16 * i, r16);
+        uint32_t left = (uint32_t)__ballot(id >= 0) & 0xffffu;
+        while (left) {
+            const int a = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
+            left &= ~(uint32_t)__ballot(id == a);
+            const int rank = lora_rank(p, a);
+            for (int r0 = 0; r0 < rank; r0 += 16) {
+                const x8 t = lora_t<T>(p, m0 + 16 * i + r16, r0, g4, id == a);
+                x8 u;
+                if constexpr (FULL) u = lora_t<T, true>(p, m0 + 16 * i + r16, r0, g4, id == a);
+#pragma unroll
+                for (int j0 = 0; j0 < NJ; j0 += 4) {
+                    x8 b[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) b[j] = lora_b<T>(p, a, rank, n0 + 16 * (j0 + j) + r16, r0, g4);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        f32x4_t d = O::mma(b[j], t, (f32x4_t){});
+                        if constexpr (FULL) d = O::mma(b[j], u, d);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[i][j0 + j][e] += id == a ? d[e] : 0.0f;
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+        }
+    }
 }
 
 }  // namespace tcm

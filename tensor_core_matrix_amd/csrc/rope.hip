@@ -12,6 +12,7 @@
 // of the workgroup, into LDS: position * inv_freq in 64 bits, reduced to one
 // turn there and only then rounded, so a position near 2^31 is as good as one
 // near 0 and no table has to be read.
+#include <stdlib.h>
 #include <type_traits>
 
 #include "layer_internal.h"
@@ -155,26 +156,33 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(RopeArgs p) {
 #pragma unroll
     for (int n = 0; n < NU; ++n) un[n] = unit_of<E, INTER>(ul + n * L, p.D, p.rot);
 
-    float x[NU][2 * E];
-    auto load = [&](int item) {
-        const int t = item / H, h = item - t * H;
-        const bool is_q = h < p.Hq, is_k = !is_q && h < p.Hq + p.Hk;
-        const HeadView& v = is_q ? p.q : is_k ? p.k : p.v;
-        const int hh = is_q ? h : is_k ? h - p.Hq : h - p.Hq - p.Hk;
-        const T* row = (const T*)v.p + (int64_t)(t0 + t) * v.ts + hh * v.hs;
+    // the heads of two items, one GROUPS after the other
+    constexpr int IN = 2;
+    float x[IN][NU][2 * E];
+    auto load = [&](int item0) {
 #pragma unroll
-        for (int n = 0; n < NU; ++n) {
-            if (un[n].live) {
-                load_e<E>(row + un[n].a, x[n]);
-                load_e<E>(row + un[n].b, x[n] + E);
-            } else {
+        for (int z = 0; z < IN; ++z) {
+            const int item = item0 + z * GROUPS;
+            if (item >= last) continue;
+            const int t = item / H, h = item - t * H;
+            const bool is_q = h < p.Hq, is_k = !is_q && h < p.Hq + p.Hk;
+            const HeadView& v = is_q ? p.q : is_k ? p.k : p.v;
+            const int hh = is_q ? h : is_k ? h - p.Hq : h - p.Hq - p.Hk;
+            const T* row = (const T*)v.p + (int64_t)(t0 + t) * v.ts + hh * v.hs;
 #pragma unroll
-                for (int i = 0; i < 2 * E; ++i) x[n][i] = 0.0f;
+            for (int n = 0; n < NU; ++n) {
+                if (un[n].live) {
+                    load_e<E>(row + un[n].a, x[z][n]);
+                    load_e<E>(row + un[n].b, x[z][n] + E);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 2 * E; ++i) x[z][n][i] = 0.0f;
+                }
             }
         }
     };
-    int item = first + group;
-    if (item < last) load(item);
+    int item0 = first + group;
+    load(item0);
     float wq[NU][2 * E], wk[NU][2 * E];
     if (p.norm) {
 #pragma unroll
@@ -189,15 +197,9 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(RopeArgs p) {
     angles(p, t0, nt, cs);
     __syncthreads();
 
-    for (; item < last; item += GROUPS) {
+    auto finish = [&](int item, float (&y)[NU][2 * E]) {
         const int t = item / H, h = item - t * H;
         const bool is_q = h < p.Hq, is_k = !is_q && h < p.Hq + p.Hk;
-        float y[NU][2 * E];
-#pragma unroll
-        for (int n = 0; n < NU; ++n)
-#pragma unroll
-            for (int i = 0; i < 2 * E; ++i) y[n][i] = x[n][i];
-        if (item + GROUPS < last) load(item + GROUPS);
         if (is_q || is_k) {
             if (p.norm) {
                 float ss = 0.0f;
@@ -233,10 +235,10 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(RopeArgs p) {
                     store_e<E>(row + un[n].a, y[n]);
                     store_e<E>(row + un[n].b, y[n] + E);
                 }
-            continue;
+            return;
         }
         const int64_t slot = p.slots[t0 + t];
-        if (slot < 0 || slot >= p.num_slots) continue;
+        if (slot < 0 || slot >= p.num_slots) return;
         const int page = (int)slot / p.page_size, at = (int)slot - page * p.page_size;
         char* row = is_k ? (char*)p.kc + page * p.k_page + at * p.k_tok + (h - p.Hq) * p.k_head
                          : (char*)p.vc + page * p.v_page + at * p.v_tok +
@@ -256,6 +258,19 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(RopeArgs p) {
                     store_e<E>((T*)row + un[n].b, y[n] + E);
                 }
             }
+    };
+    for (; item0 < last; item0 += IN * GROUPS) {
+        float y[IN][NU][2 * E];
+#pragma unroll
+        for (int z = 0; z < IN; ++z)
+#pragma unroll
+            for (int n = 0; n < NU; ++n)
+#pragma unroll
+                for (int i = 0; i < 2 * E; ++i) y[z][n][i] = x[z][n][i];
+        load(item0 + IN * GROUPS);
+#pragma unroll
+        for (int z = 0; z < IN; ++z)
+            if (item0 + z * GROUPS < last) finish(item0 + z * GROUPS, y[z]);
     }
 }
 
@@ -428,10 +443,14 @@ hipError_t forward(RopeArgs a, bool inter, hipStream_t st) {
     return by_shape(a.D, a.rot, inter, [&](auto L, auto E, auto NU, auto INTER) {
         constexpr int groups = 256 / decltype(L)::value;
         const int H = a.Hq + a.Hk + a.Hv;
-        // tokens a workgroup: until its items fill its lanes, while there are
-        // workgroups enough for every compute unit
+        // tokens a workgroup: as many as leave eight workgroups for every compute
+        // unit (a workgroup's first reads and angles take about as long as the
+        // reads of three of its rounds); with small heads until its items fill its lanes, while every
+        // compute unit has a workgroup
         a.tb = 1;
-        while (a.tb * H < groups && 2 * a.tb * (a.rot / 2) <= kRopeTrig && cdiv_i(a.T, 2 * a.tb) >= 256)
+        const int wgs = getenv("RW") ? atoi(getenv("RW")) : 2048;
+        while (2 * a.tb * (a.rot / 2) <= kRopeTrig &&
+               cdiv_i(a.T, 2 * a.tb) >= (a.tb * H < groups ? 256 : wgs))
             a.tb *= 2;
         // few workgroups: a token block's heads are spread over several
         const int steps = cdiv_i((int64_t)a.tb * H, groups), blocks = cdiv_i(a.T, a.tb);
