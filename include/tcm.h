@@ -401,7 +401,8 @@ typedef enum tcm_rope_layout {
  *   head_dim  D, a multiple of 8, at most 256 (TCM_ERR_UNSUPPORTED_SHAPE)
  *   rot_dim   even, 0 .. D (TCM_ERR_INVALID_SHAPE)
  *   positions T int32;  inv_freq  rot_dim / 2 doubles (both NULL if rot_dim == 0)
- *   q_weight, k_weight  D elements of weight_dtype: TCM_F32 or the call's dtype
+ *   q_weight, k_weight  D elements of weight_dtype: TCM_F32 or the call's dtype,
+ *             16-byte aligned (TCM_ERR_MISALIGNED)
  */
 typedef struct tcm_rope {
     int64_t head_dim, rot_dim;

@@ -91,6 +91,13 @@ tcm_status check_cache(const tcm_cache* c, tcm_dtype dtype, int64_t Hk, int64_t 
     return TCM_OK;
 }
 
+// log2 of a power of two, -1 of any other page size
+int32_t shift_of(int64_t page_size) {
+    for (int32_t i = 0; i <= 20; ++i)
+        if (page_size == int64_t(1) << i) return i;
+    return -1;
+}
+
 // ---- norm and rotation -------------------------------------------------------------
 
 tcm_status check_rope(const tcm_rope* r, tcm_dtype dtype, int64_t T, int64_t Hq, int64_t Hk) {
@@ -107,6 +114,7 @@ tcm_status check_rope(const tcm_rope* r, tcm_dtype dtype, int64_t T, int64_t Hq,
         return TCM_ERR_UNSUPPORTED_SHAPE;
     if (T > 0 && Hq + Hk > 0 && r->rot_dim > 0 && (!r->positions || !r->inv_freq))
         return TCM_ERR_NULL_POINTER;
+    if (weighted && (!aligned16(r->q_weight) || !aligned16(r->k_weight))) return TCM_ERR_MISALIGNED;
     return TCM_OK;
 }
 
@@ -125,6 +133,7 @@ void fill_rope(RopeArgs* a, const tcm_rope* r, int64_t T, int64_t Hq, int64_t Hk
     a->rot = (int32_t)r->rot_dim;
     a->norm = r->norm != 0;
     a->w_f32 = r->weight_dtype == TCM_F32;
+    a->inv_d = 1.0f / (float)r->head_dim;
 }
 
 int64_t bwd_workspace(int64_t D) { return int64_t(kRopeBwdGrid) * 2 * D * 4; }
@@ -309,6 +318,7 @@ tcm_status tcm_qk_norm_rope_cache(const tcm_heads* q, const tcm_heads* k, const 
     a.slots = slots;
     a.num_slots = cache->pages * cache->page_size;
     a.page_size = (int32_t)cache->page_size;
+    a.page_shift = shift_of(cache->page_size);
     a.cache_e4m3 = cache->dtype == TCM_E4M3;
     const int64_t es = a.cache_e4m3 ? 1 : 2;
     a.kc = cache->k;
@@ -439,9 +449,7 @@ tcm_status tcm_paged_attention(const tcm_heads* q, const tcm_cache* cache,
     a.D = (int32_t)D;
     a.pages = (int32_t)cache->pages;
     a.page_size = (int32_t)cache->page_size;
-    a.page_shift = -1;
-    for (int i = 0; i <= 20; ++i)
-        if (cache->page_size == int64_t(1) << i) a.page_shift = i;
+    a.page_shift = shift_of(cache->page_size);
     a.max_len = (int32_t)max_len;
     a.window = window > max_len ? 0 : (int32_t)window;
     a.chunk = (int32_t)sp.chunk;

@@ -36,6 +36,8 @@ struct RopeArgs {
     const int32_t* slots;
     int64_t num_slots;
     int32_t page_size, cache_e4m3;
+    int32_t page_shift;  // log2 of page_size where it is a power of two, else -1
+    float inv_d;         // 1 / D
     int64_t k_page, k_tok, k_head, v_page, v_tok, v_head;  // bytes
     void* kc;
     void* vc;
@@ -47,6 +49,7 @@ struct RopeArgs {
 };
 
 constexpr int kRopeTrig = 1024;      // (token, pair) angles of one workgroup
+constexpr int kRopeTokens = 64;      // tokens of one workgroup, at most
 constexpr int kRopeBwdGrid = 1024;   // workgroups of the backward pass
 
 hipError_t launch_norm_rope(const RopeArgs& a, int32_t dtype, int32_t layout, hipStream_t st);

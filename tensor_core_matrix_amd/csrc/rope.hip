@@ -6,13 +6,14 @@
 // is read once and written once.  L lanes hold one head, 2 E elements each: E
 // at `a` and E at `b`, chosen so that a lane holds whole pairs (half layout:
 // a = E u, b = rot / 2 + E u; interleaved: 2 E consecutive elements), so the
-// rotation needs no other lane and the norm one sum over L lanes.  With E = 4
-// every access is 8 bytes and a head's two halves are contiguous over its
-// lanes.  The angles of a workgroup's tokens are computed once, by the threads
+// rotation needs no other lane and the norm one sum over L lanes.  With E = 8
+// every access is 16 bytes and a head's two halves are contiguous over its
+// lanes; and as what is done once a head and lane -- the sum, the root, the
+// addresses -- is half of the instructions, few lanes a head count as much
+// (8191 tokens of 32 + 8 + 8 heads of 128, E4M3 cache: 43 us, and 77 with E = 4).  The angles of a workgroup's tokens are computed once, by the threads
 // of the workgroup, into LDS: position * inv_freq in 64 bits, reduced to one
 // turn there and only then rounded, so a position near 2^31 is as good as one
 // near 0 and no table has to be read.
-#include <stdlib.h>
 #include <type_traits>
 
 #include "layer_internal.h"
@@ -25,32 +26,35 @@ namespace {
 template <class T>
 __device__ __forceinline__ float to_f(T x) { return (float)x; }
 
-// E elements at p (E == 4: one 8-byte access)
+// E elements at p in one access
 template <int E, class T>
 __device__ __forceinline__ void load_e(const T* p, float* x) {
-    if constexpr (E == 4) {
-        typedef T t4 __attribute__((ext_vector_type(4)));
-        const t4 v = *(const t4*)p;
+    typedef T vec __attribute__((ext_vector_type(E)));
+    const vec v = *(const vec*)p;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = (float)v[i];
-    } else {
-        x[0] = (float)p[0];
-    }
+    for (int i = 0; i < E; ++i) x[i] = (float)v[i];
 }
 template <int E, class T>
 __device__ __forceinline__ void store_e(T* p, const float* x) {
-    if constexpr (E == 4) {
-        store4<T>(p, x[0], x[1], x[2], x[3]);
-    } else {
-        p[0] = convert_out<T>(x[0]);
-    }
+    typedef T vec __attribute__((ext_vector_type(E)));
+    vec v;
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] = convert_out<T>(x[i]);
+    *(vec*)p = v;
 }
 // E elements of a weight (fp32 or T); ones where there is none
 template <int E, class T>
 __device__ __forceinline__ void load_w(const void* w, int f32, int at, float* x) {
+    if (!w) {
 #pragma unroll
-    for (int i = 0; i < E; ++i)
-        x[i] = !w ? 1.0f : f32 ? ((const float*)w)[at + i] : (float)((const T*)w)[at + i];
+        for (int i = 0; i < E; ++i) x[i] = 1.0f;
+    } else if (!f32) {
+        load_e<E>((const T*)w + at, x);
+    } else {
+        constexpr int V = E < 4 ? E : 4;
+#pragma unroll
+        for (int i = 0; i < E; i += V) load_e<V>((const float*)w + at + i, x + i);
+    }
 }
 
 // E4M3 of x, saturated at +-448, NaN kept
@@ -59,12 +63,18 @@ __device__ __forceinline__ float e4m3_range(float x) {
 }
 template <int E>
 __device__ __forceinline__ void store_e4m3(unsigned char* p, const float* x) {
-    if constexpr (E == 4) {
-        int v = __builtin_amdgcn_cvt_pk_fp8_f32(e4m3_range(x[0]), e4m3_range(x[1]), 0, false);
-        v = __builtin_amdgcn_cvt_pk_fp8_f32(e4m3_range(x[2]), e4m3_range(x[3]), v, true);
-        *(int*)p = v;
-    } else {
+    if constexpr (E == 1) {
         p[0] = (unsigned char)__builtin_amdgcn_cvt_pk_fp8_f32(e4m3_range(x[0]), 0.0f, 0, false);
+    } else {
+        typedef int vec __attribute__((ext_vector_type(E / 4)));
+        vec v;
+#pragma unroll
+        for (int i = 0; i < E / 4; ++i) {
+            const float* y = x + 4 * i;
+            const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(e4m3_range(y[0]), e4m3_range(y[1]), 0, false);
+            v[i] = __builtin_amdgcn_cvt_pk_fp8_f32(e4m3_range(y[2]), e4m3_range(y[3]), lo, true);
+        }
+        *(vec*)p = v;
     }
 }
 
@@ -79,11 +89,19 @@ template <int L>
 __device__ __forceinline__ float head_sum(float x) {
     x += dpp<0xB1>(x);              // lanes 1, 0, 3, 2 of a quad
     x += dpp<0x4E>(x);              // 2, 3, 0, 1
-    x += dpp<0x141>(x);             // mirrored within 8
+    if constexpr (L >= 8) x += dpp<0x141>(x);   // mirrored within 8
     if constexpr (L >= 16) x += dpp<0x140>(x);  // mirrored within 16
     if constexpr (L >= 32) x += __shfl_xor(x, 16);
     if constexpr (L >= 64) x += __shfl_xor(x, 32);
     return x;
+}
+
+// 1 / sqrt(x): the hardware's approximation (1 ulp) and one Newton step
+__device__ __forceinline__ float inv_sqrt(float x) {
+    const float r = __builtin_amdgcn_rsqf(x);
+    const float e = 0.5f - 0.5f * x * r * r;
+    // (zero, infinite and NaN x have no step)
+    return e == e ? r + r * e : r;
 }
 
 // The unit u of a head: where its elements are, and the first of its pairs.
@@ -117,18 +135,34 @@ __device__ __forceinline__ void angles(const RopeArgs& p, int t0, int nt, float 
     }
 }
 
+// E floats of LDS at a multiple of E, in 16-byte reads where E allows
+template <int E>
+__device__ __forceinline__ void lds_floats(const float* p, float* x) {
+    if constexpr (E % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < E / 4; ++i) {
+            const f32x4_t v = *(const f32x4_t*)(p + 4 * i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[4 * i + j] = v[j];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) x[i] = p[i];
+    }
+}
+
 // (a, b) turned by the angles c + i s; sign -1 turns back
 template <int E, bool INTER>
 __device__ __forceinline__ void turn(float* a, float* b, const float* c, const float* s, float sign) {
-    if constexpr (INTER && E == 4) {
+    if constexpr (INTER && E > 1) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < E / 2; ++i) {
             const float x = a[2 * i], y = a[2 * i + 1], sn = sign * s[i];
             a[2 * i] = x * c[i] - y * sn;
             a[2 * i + 1] = y * c[i] + x * sn;
-            const float z = b[2 * i], w = b[2 * i + 1], sm = sign * s[2 + i];
-            b[2 * i] = z * c[2 + i] - w * sm;
-            b[2 * i + 1] = w * c[2 + i] + z * sm;
+            const float z = b[2 * i], w = b[2 * i + 1], sm = sign * s[E / 2 + i];
+            b[2 * i] = z * c[E / 2 + i] - w * sm;
+            b[2 * i + 1] = w * c[E / 2 + i] + z * sm;
         }
     } else {
 #pragma unroll
@@ -140,138 +174,139 @@ __device__ __forceinline__ void turn(float* a, float* b, const float* c, const f
     }
 }
 
+// (token, head) of an item, and of the one GROUPS further: no division a step
+struct Item {
+    int t, h;
+    __device__ __forceinline__ Item(int item, int H) : t(item / H), h(item - item / H * H) {}
+    __device__ __forceinline__ void step(int by, int H) {
+        h += by;
+        while (h >= H) h -= H, ++t;
+    }
+};
+
 // ---- forward ------------------------------------------------------------------
-// A workgroup takes p.tb tokens and, of their (token, head) items, p.per; 256 / L
-// at a time, the next ones being loaded while these are computed.
+// A workgroup takes p.tb tokens and, of their items -- query heads of all tokens, then
+// key heads, then value heads -- p.per; 256 / L at a time, the next ones being loaded
+// while these are computed.
 template <class T, int L, int E, int NU, bool INTER>
 __global__ __launch_bounds__(256) void norm_rope_kernel(RopeArgs p) {
-    __shared__ float cs[2][kRopeTrig];
+    __shared__ __attribute__((aligned(16))) float cs[2][kRopeTrig];
+    // the tokens' places in the cache (read beside the heads, a slot would be
+    // waited for with all the reads that went out before it)
+    __shared__ int32_t slot_of[kRopeTokens];
     constexpr int GROUPS = 256 / L;
     const int group = threadIdx.x / L, ul = threadIdx.x % L;
     const int t0 = blockIdx.x * p.tb, nt = min(p.tb, p.T - t0);
     const int H = p.Hq + p.Hk + p.Hv;
     const int first = blockIdx.y * p.per, last = min(nt * H, first + p.per);
     if (first >= last) return;
+    if (p.slots && threadIdx.x < nt) slot_of[threadIdx.x] = p.slots[t0 + threadIdx.x];
+    angles(p, t0, nt, cs);
+    __syncthreads();
     Unit un[NU];
 #pragma unroll
     for (int n = 0; n < NU; ++n) un[n] = unit_of<E, INTER>(ul + n * L, p.D, p.rot);
 
-    // the heads of two items, one GROUPS after the other
-    constexpr int IN = 2;
-    float x[IN][NU][2 * E];
-    auto load = [&](int item0) {
+    // 0 query, 1 key, 2 value heads; items from `base` on
+    auto heads = [&](auto WHICH, int base) {
+        constexpr int which = decltype(WHICH)::value;
+        const int Hw = which == 0 ? p.Hq : which == 1 ? p.Hk : p.Hv;
+        const HeadView& v = which == 0 ? p.q : which == 1 ? p.k : p.v;
+        const int from = max(first, base) - base, to = min(last, base + nt * Hw) - base;
+        if (from + group >= to) return;
+        float w[NU][2 * E];
+        if (which < 2 && p.norm)
 #pragma unroll
-        for (int z = 0; z < IN; ++z) {
-            const int item = item0 + z * GROUPS;
-            if (item >= last) continue;
-            const int t = item / H, h = item - t * H;
-            const bool is_q = h < p.Hq, is_k = !is_q && h < p.Hq + p.Hk;
-            const HeadView& v = is_q ? p.q : is_k ? p.k : p.v;
-            const int hh = is_q ? h : is_k ? h - p.Hq : h - p.Hq - p.Hk;
-            const T* row = (const T*)v.p + (int64_t)(t0 + t) * v.ts + hh * v.hs;
+            for (int n = 0; n < NU; ++n)
+                if (un[n].live) {
+                    load_w<E, T>(which ? p.wk : p.wq, p.w_f32, un[n].a, w[n]);
+                    load_w<E, T>(which ? p.wk : p.wq, p.w_f32, un[n].b, w[n] + E);
+                }
+        float x[NU][2 * E];
+        auto load = [&](const Item& it) {
+            const T* row = (const T*)v.p + (int64_t)(t0 + it.t) * v.ts + it.h * v.hs;
 #pragma unroll
             for (int n = 0; n < NU; ++n) {
                 if (un[n].live) {
-                    load_e<E>(row + un[n].a, x[z][n]);
-                    load_e<E>(row + un[n].b, x[z][n] + E);
+                    load_e<E>(row + un[n].a, x[n]);
+                    load_e<E>(row + un[n].b, x[n] + E);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 2 * E; ++i) x[z][n][i] = 0.0f;
+                    for (int i = 0; i < 2 * E; ++i) x[n][i] = 0.0f;
                 }
             }
-        }
-    };
-    int item0 = first + group;
-    load(item0);
-    float wq[NU][2 * E], wk[NU][2 * E];
-    if (p.norm) {
-#pragma unroll
-        for (int n = 0; n < NU; ++n)
-            if (un[n].live) {
-                load_w<E, T>(p.wq, p.w_f32, un[n].a, wq[n]);
-                load_w<E, T>(p.wq, p.w_f32, un[n].b, wq[n] + E);
-                load_w<E, T>(p.wk, p.w_f32, un[n].a, wk[n]);
-                load_w<E, T>(p.wk, p.w_f32, un[n].b, wk[n] + E);
-            }
-    }
-    angles(p, t0, nt, cs);
-    __syncthreads();
-
-    auto finish = [&](int item, float (&y)[NU][2 * E]) {
-        const int t = item / H, h = item - t * H;
-        const bool is_q = h < p.Hq, is_k = !is_q && h < p.Hq + p.Hk;
-        if (is_q || is_k) {
-            if (p.norm) {
-                float ss = 0.0f;
-#pragma unroll
-                for (int n = 0; n < NU; ++n)
-#pragma unroll
-                    for (int i = 0; i < 2 * E; ++i) ss += y[n][i] * y[n][i];
-                ss = head_sum<L>(ss);
-                const float r = 1.0f / sqrtf(ss / (float)p.D + p.eps);
-#pragma unroll
-                for (int n = 0; n < NU; ++n)
-#pragma unroll
-                    for (int i = 0; i < 2 * E; ++i) y[n][i] *= r * (is_q ? wq[n][i] : wk[n][i]);
-            }
+        };
+        Item it(from + group, Hw);
+        load(it);
+        for (int i0 = from + group; i0 < to; i0 += GROUPS) {
+            float y[NU][2 * E];
 #pragma unroll
             for (int n = 0; n < NU; ++n)
-                if (un[n].turn) {
-                    float c[E], s[E];
 #pragma unroll
-                    for (int i = 0; i < E; ++i) {
-                        c[i] = cs[0][t * (p.rot >> 1) + un[n].f + i];
-                        s[i] = cs[1][t * (p.rot >> 1) + un[n].f + i];
-                    }
-                    turn<E, INTER>(y[n], y[n] + E, c, s, 1.0f);
+                for (int i = 0; i < 2 * E; ++i) y[n][i] = x[n][i];
+            const Item now = it;
+            it.step(GROUPS, Hw);
+            if (i0 + GROUPS < to) load(it);
+            if (which < 2) {
+                if (p.norm) {
+                    float ss = 0.0f;
+#pragma unroll
+                    for (int n = 0; n < NU; ++n)
+#pragma unroll
+                        for (int i = 0; i < 2 * E; ++i) ss += y[n][i] * y[n][i];
+                    const float r = inv_sqrt(head_sum<L>(ss) * p.inv_d + p.eps);
+#pragma unroll
+                    for (int n = 0; n < NU; ++n)
+#pragma unroll
+                        for (int i = 0; i < 2 * E; ++i) y[n][i] *= r * w[n][i];
                 }
-        }
-        if (is_q || !p.slots) {
-            const HeadView& o = is_q ? p.qo : p.ko;
-            T* row = (T*)o.p + (int64_t)(t0 + t) * o.ts + (is_q ? h : h - p.Hq) * o.hs;
+#pragma unroll
+                for (int n = 0; n < NU; ++n)
+                    if (un[n].turn) {
+                        float c[E], sn[E];
+                        const int at = now.t * (p.rot >> 1) + un[n].f;
+                        lds_floats<E>(&cs[0][at], c);
+                        lds_floats<E>(&cs[1][at], sn);
+                        turn<E, INTER>(y[n], y[n] + E, c, sn, 1.0f);
+                    }
+            }
+            if (which == 0 || !p.slots) {
+                const HeadView& o = which ? p.ko : p.qo;
+                T* row = (T*)o.p + (int64_t)(t0 + now.t) * o.ts + now.h * o.hs;
+#pragma unroll
+                for (int n = 0; n < NU; ++n)
+                    if (un[n].live) {
+                        store_e<E>(row + un[n].a, y[n]);
+                        store_e<E>(row + un[n].b, y[n] + E);
+                    }
+                continue;
+            }
+            const int64_t slot = slot_of[now.t];
+            if (slot < 0 || slot >= p.num_slots) continue;
+            const int page = p.page_shift >= 0 ? (int)slot >> p.page_shift : (int)slot / p.page_size;
+            const int at = (int)slot - page * p.page_size;
+            char* row = which == 1 ? (char*)p.kc + page * p.k_page + at * p.k_tok + now.h * p.k_head
+                                   : (char*)p.vc + page * p.v_page + at * p.v_tok + now.h * p.v_head;
+            const float inv = which == 1 ? p.k_inv : p.v_inv;
 #pragma unroll
             for (int n = 0; n < NU; ++n)
                 if (un[n].live) {
-                    store_e<E>(row + un[n].a, y[n]);
-                    store_e<E>(row + un[n].b, y[n] + E);
+                    if (p.cache_e4m3) {
+                        float z[2 * E];
+#pragma unroll
+                        for (int i = 0; i < 2 * E; ++i) z[i] = y[n][i] * inv;
+                        store_e4m3<E>((unsigned char*)row + un[n].a, z);
+                        store_e4m3<E>((unsigned char*)row + un[n].b, z + E);
+                    } else {
+                        store_e<E>((T*)row + un[n].a, y[n]);
+                        store_e<E>((T*)row + un[n].b, y[n] + E);
+                    }
                 }
-            return;
         }
-        const int64_t slot = p.slots[t0 + t];
-        if (slot < 0 || slot >= p.num_slots) return;
-        const int page = (int)slot / p.page_size, at = (int)slot - page * p.page_size;
-        char* row = is_k ? (char*)p.kc + page * p.k_page + at * p.k_tok + (h - p.Hq) * p.k_head
-                         : (char*)p.vc + page * p.v_page + at * p.v_tok +
-                               (h - p.Hq - p.Hk) * p.v_head;
-        const float inv = is_k ? p.k_inv : p.v_inv;
-#pragma unroll
-        for (int n = 0; n < NU; ++n)
-            if (un[n].live) {
-                if (p.cache_e4m3) {
-                    float z[2 * E];
-#pragma unroll
-                    for (int i = 0; i < 2 * E; ++i) z[i] = y[n][i] * inv;
-                    store_e4m3<E>((unsigned char*)row + un[n].a, z);
-                    store_e4m3<E>((unsigned char*)row + un[n].b, z + E);
-                } else {
-                    store_e<E>((T*)row + un[n].a, y[n]);
-                    store_e<E>((T*)row + un[n].b, y[n] + E);
-                }
-            }
     };
-    for (; item0 < last; item0 += IN * GROUPS) {
-        float y[IN][NU][2 * E];
-#pragma unroll
-        for (int z = 0; z < IN; ++z)
-#pragma unroll
-            for (int n = 0; n < NU; ++n)
-#pragma unroll
-                for (int i = 0; i < 2 * E; ++i) y[z][n][i] = x[z][n][i];
-        load(item0 + IN * GROUPS);
-#pragma unroll
-        for (int z = 0; z < IN; ++z)
-            if (item0 + z * GROUPS < last) finish(item0 + z * GROUPS, y[z]);
-    }
+    heads(std::integral_constant<int, 0>{}, 0);
+    heads(std::integral_constant<int, 1>{}, nt * p.Hq);
+    if (p.Hv > 0) heads(std::integral_constant<int, 2>{}, nt * (p.Hq + p.Hk));
 }
 
 // ---- backward -----------------------------------------------------------------
@@ -284,7 +319,7 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(RopeArgs p) {
 // norm_rope_dw_kernel, in a fixed order both.
 template <class T, int L, int E, int NU, bool INTER>
 __global__ __launch_bounds__(256) void norm_rope_bwd_kernel(RopeArgs p) {
-    __shared__ float cs[2][2][kRopeTrig];
+    __shared__ __attribute__((aligned(16))) float cs[2][2][kRopeTrig];
     constexpr int GROUPS = 256 / L;
     __shared__ float join[256 * 2 * E * NU];
     const int group = threadIdx.x / L, ul = threadIdx.x % L;
@@ -310,8 +345,10 @@ __global__ __launch_bounds__(256) void norm_rope_bwd_kernel(RopeArgs p) {
         const HeadView& xv = which ? p.k : p.q;
         const HeadView& dyv = which ? p.dko : p.dqo;
         const HeadView& dxv = which ? p.ko : p.qo;
-        for (int item = group; item < nt * H; item += GROUPS) {
-            const int t = item / H, h = item - t * H;
+        if (group >= nt * H) return;
+        Item it(group, H);
+        for (int item = group; item < nt * H; item += GROUPS, it.step(GROUPS, H)) {
+            const int t = it.t, h = it.h;
             const T* xr = (const T*)xv.p + (int64_t)(t0 + t) * xv.ts + h * xv.hs;
             const T* dyr = (const T*)dyv.p + (int64_t)(t0 + t) * dyv.ts + h * dyv.hs;
             float x[NU][2 * E], dy[NU][2 * E];
@@ -331,11 +368,9 @@ __global__ __launch_bounds__(256) void norm_rope_bwd_kernel(RopeArgs p) {
                 }
                 if (un[n].turn) {
                     float c[E], s[E];
-#pragma unroll
-                    for (int i = 0; i < E; ++i) {
-                        c[i] = c2[0][t * (p.rot >> 1) + un[n].f + i];
-                        s[i] = c2[1][t * (p.rot >> 1) + un[n].f + i];
-                    }
+                    const int at = t * (p.rot >> 1) + un[n].f;
+                    lds_floats<E>(&c2[0][at], c);
+                    lds_floats<E>(&c2[1][at], s);
                     turn<E, INTER>(dy[n], dy[n] + E, c, s, -1.0f);
                 }
             }
@@ -349,8 +384,8 @@ __global__ __launch_bounds__(256) void norm_rope_bwd_kernel(RopeArgs p) {
                     }
                 ss = head_sum<L>(ss);
                 gx = head_sum<L>(gx);
-                const float r = 1.0f / sqrtf(ss / (float)p.D + p.eps);
-                const float m = r * r * gx / (float)p.D;  // mean(g h) r
+                const float r = inv_sqrt(ss * p.inv_d + p.eps);
+                const float m = r * r * gx * p.inv_d;  // mean(g h) r
 #pragma unroll
                 for (int n = 0; n < NU; ++n)
 #pragma unroll
@@ -422,9 +457,13 @@ __global__ __launch_bounds__(256) void norm_rope_dw_kernel(const float* partial,
 
 int cdiv_i(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
-// f(lanes, elements, units, layout) of the instance for these sizes: E = 4 where
-// pairs come in groups of four (rot_dim a multiple of 8), else pair by pair.
-template <class F>
+// f(lanes, elements, units, layout) of the instance for these sizes: E = 8 where
+// pairs and what is not rotated come in groups of eight (rot_dim and head_dim
+// multiples of 16), E = 4 where pairs come in fours, else pair by pair.
+// (WIDE: E = 8 is for the forward pass; the backward one keeps twice the heads and
+// the weights' sums in registers, and takes 69 us with it and 58 without for 8192
+// tokens of 32 + 8 heads of 128.)
+template <bool WIDE, class F>
 hipError_t by_shape(int D, int rot, bool inter, F&& f) {
     auto with = [&](auto L, auto E, auto NU) {
         return inter ? f(L, E, NU, std::true_type{}) : f(L, E, NU, std::false_type{});
@@ -432,25 +471,33 @@ hipError_t by_shape(int D, int rot, bool inter, F&& f) {
     std::integral_constant<int, 1> i1;
     std::integral_constant<int, 2> i2;
     std::integral_constant<int, 4> i4;
+    std::integral_constant<int, 8> i8;
+    if constexpr (WIDE) {
+        if (rot % 16 == 0 && D % 16 == 0) {
+            if (D <= 64) return with(i4, i8, i1);
+            if (D <= 128) return with(i8, i8, i1);
+            return with(std::integral_constant<int, 16>{}, i8, i1);
+        }
+    }
     if (rot % 8 != 0) return with(std::integral_constant<int, 64>{}, i1, i2);
-    if (D <= 64) return with(std::integral_constant<int, 8>{}, i4, i1);
+    if (D <= 64) return with(i8, i4, i1);
     if (D <= 128) return with(std::integral_constant<int, 16>{}, i4, i1);
     return with(std::integral_constant<int, 32>{}, i4, i1);
 }
 
 template <class T>
 hipError_t forward(RopeArgs a, bool inter, hipStream_t st) {
-    return by_shape(a.D, a.rot, inter, [&](auto L, auto E, auto NU, auto INTER) {
+    return by_shape<true>(a.D, a.rot, inter, [&](auto L, auto E, auto NU, auto INTER) {
         constexpr int groups = 256 / decltype(L)::value;
         const int H = a.Hq + a.Hk + a.Hv;
-        // tokens a workgroup: as many as leave eight workgroups for every compute
-        // unit (a workgroup's first reads and angles take about as long as the
-        // reads of three of its rounds); with small heads until its items fill its lanes, while every
-        // compute unit has a workgroup
+        // Tokens a workgroup: as many as leave four workgroups for every compute
+        // unit, since each begins with the angles and its first reads (8191 tokens
+        // of 32 + 8 + 8 heads of 128: 47 us, 53 with eight, 60 with 16 and 50 with two);
+        // with small heads until its items fill its lanes, while every compute unit
+        // has a workgroup.
         a.tb = 1;
-        const int wgs = getenv("RW") ? atoi(getenv("RW")) : 2048;
-        while (2 * a.tb * (a.rot / 2) <= kRopeTrig &&
-               cdiv_i(a.T, 2 * a.tb) >= (a.tb * H < groups ? 256 : wgs))
+        while (2 * a.tb * (a.rot / 2) <= kRopeTrig && 2 * a.tb <= kRopeTokens &&
+               cdiv_i(a.T, 2 * a.tb) >= (a.tb * H < groups ? 256 : 1024))
             a.tb *= 2;
         // few workgroups: a token block's heads are spread over several
         const int steps = cdiv_i((int64_t)a.tb * H, groups), blocks = cdiv_i(a.T, a.tb);
@@ -467,7 +514,7 @@ hipError_t forward(RopeArgs a, bool inter, hipStream_t st) {
 
 template <class T>
 hipError_t backward(RopeArgs a, bool inter, hipStream_t st) {
-    return by_shape(a.D, a.rot, inter, [&](auto L, auto E, auto NU, auto INTER) {
+    return by_shape<false>(a.D, a.rot, inter, [&](auto L, auto E, auto NU, auto INTER) {
         constexpr int groups = 256 / decltype(L)::value;
         // tokens a step: until the key heads of a block fill the lanes too,
         // while there are steps enough for every workgroup's first

@@ -95,7 +95,8 @@ def test_rope_refusals():
                dict(r=rope(freq=None))):
         assert fwd(**kw) == NULLP, kw
     assert fwd(r=rope(rot=0, pos=None, freq=None)) in PASSED
-    for kw in (dict(q=heads(P[0] + 8)), dict(k=heads(ts=516)), dict(qo=heads(hs=68))):
+    for kw in (dict(q=heads(P[0] + 8)), dict(k=heads(ts=516)), dict(qo=heads(hs=68)), dict(r=rope(wq=P[10] + 2)),
+               dict(r=rope(wk=P[10] + 8))):
         assert fwd(**kw) == MISALIGNED, kw
     assert fwd(T=0, q=None, k=None, qo=None, ko=None) == OK
     assert fwd(Hq=0, q=None, qo=None) in PASSED and fwd(Hk=0, k=None, ko=None) in PASSED
