@@ -344,7 +344,7 @@ tcm_status tcm_plan_gemm(int64_t batch, int64_t M, int64_t N, int64_t K, tcm_dty
  * do not reach the rows of another.
  * R a multiple of 8, at most 128; K a multiple of 8 (TCM_ERR_MISALIGNED
  * otherwise); ldx a multiple of 8 and at most 2^21; X, W, A, B and Out 16-byte
- * aligned.  L == 0 or R == 0 gives the projection alone.
+ * aligned; Out overlaps no input.  L == 0 or R == 0 gives the projection alone.
  */
 tcm_status tcm_lora_gemm_tn(const void* X, int64_t ldx, const void* W, const void* A,
                             const void* B, const int32_t* row_adapter, const int32_t* ranks,

@@ -414,7 +414,8 @@ tcm_status tcm_paged_attention(const tcm_heads* q, const tcm_cache* cache,
     if (cache->pages == 0) max_len = 0;
     // the first tile of a window begins up to 31 keys before it
     const int64_t span = window > 0 && window + 31 < max_len ? window + 31 : max_len;
-    Split sp = split_of(B, Hq, Hk, span);
+    const Split sp = split_of(B, Hq, Hk, span);
+    if (B * Hk * cdiv(Hq / Hk, 16) > INT32_MAX / sp.n) return TCM_ERR_UNSUPPORTED_SHAPE;  // workgroups
     if (sp.n > 1) {
         if (!workspace) return TCM_ERR_NULL_POINTER;
         if (!aligned16(workspace)) return TCM_ERR_MISALIGNED;
@@ -440,8 +441,10 @@ tcm_status tcm_paged_attention(const tcm_heads* q, const tcm_cache* cache,
     a.table_stride = table_stride;
     a.lengths = lengths;
     a.lse = lse;
-    a.po = (float*)workspace;
-    a.pml = a.po + B * Hq * sp.n * D;
+    if (sp.n > 1) {
+        a.po = (float*)workspace;
+        a.pml = a.po + B * Hq * sp.n * D;
+    }
     a.B = (int32_t)B;
     a.Hq = (int32_t)Hq;
     a.Hk = (int32_t)Hk;

@@ -316,18 +316,26 @@ __global__ __launch_bounds__(1024) void lora_rows_kernel(LoraArgs p) {
 // ---- many rows ----------------------------------------------------------------------
 // BM x BN tiles, WM x WN waves, 64-deep slices by DMA into a ring of S stages (128-byte
 // rows whose 16-byte chunk c lies at c ^ (row / 2) % 8, so that 16 rows' reads meet 16
-// bank groups), one barrier a slice.
-template <class T, class TO, int BM, int BN, int S, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN, 2) void lora_tile_kernel(LoraArgs p, int tiles_m, int tiles_n) {
+// bank groups), one barrier a slice.  Where tiles are small, KG such groups of waves,
+// each with a ring, take every KG-th slice side by side and their sums meet in LDS,
+// so that one group's products and reads cover another's wait and barrier (without
+// adapters, 128 rows of 4096 x 4096 in 64 x 64 tiles: 21 us with one group, 17 with two;
+// 333 rows in 128 x 64 tiles: 26 and 25).  A compute unit then reads about 65 GB/s into
+// LDS, in tiles of any size, rings of any depth: that is the bound of these.
+template <class T, class TO, int BM, int BN, int S, int WM, int WN, int KG>
+__global__ __launch_bounds__(64 * WM * WN * KG, 2) void lora_tile_kernel(LoraArgs p, int tiles_m, int tiles_n) {
     typedef LoraMma<T> O;
     typedef typename O::x8 x8;
     constexpr int WV = WM * WN, ROWS = 8 * WV;  // rows of one copy by all waves
     constexpr int STAGE = (BM + BN) * 128, CA = BM / ROWS, CB = BN / ROWS, C = CA + CB;
     constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
     static_assert((ROWS / 2) % 8 == 0 || ROWS % 16 == 0, "a lane's chunk is the same in every copy");
-    __shared__ __attribute__((aligned(1024))) char lds[S * STAGE];
+    __shared__ __attribute__((aligned(1024))) char all[KG * S * STAGE];
+    static_assert(KG == 1 || (KG - 1) * BM * BN * 4 <= KG * S * STAGE, "the groups' sums meet in the rings");
     const int lane = threadIdx.x & 63, r16 = lane & 15, g4 = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int kg = wave_all / WV, wave = wave_all % WV;
+    char* const lds = all + kg * S * STAGE;
     const int wm = wave / WN, wn = wave % WN;
     // tiles down groups of 4 tile rows, neighbours on one XCD
     GemmArgs order;
@@ -345,10 +353,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void lora_tile_kernel(LoraArgs p, 
         make_rsrc((const char*)p.W + (int64_t)tn * BN * ldb, (uint32_t)rows_b * ldb);
     const int cp_row = wave * 8 + lane / 8;
     const int cp_chunk = (lane & 7) ^ ((cp_row >> 1) & 7);
-    const int ksteps = (p.K + 63) / 64;
+    const int ksteps = (p.K + 64 * KG - 1) / (64 * KG);  // slices of each group
     auto issue = [&](int g) {
-        const bool in = g < ksteps && g * 64 + cp_chunk * 8 < p.K;
-        const uint32_t at = (uint32_t)g * 128u + (uint32_t)cp_chunk * 16u;
+        const int slice = g * KG + kg;
+        const bool in = g < ksteps && slice * 64 + cp_chunk * 8 < p.K;
+        const uint32_t at = (uint32_t)slice * 128u + (uint32_t)cp_chunk * 16u;
         char* dst = lds + (g % S) * STAGE + wave * 1024;
 #pragma unroll
         for (int x = 0; x < CA; ++x)
@@ -394,10 +403,29 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void lora_tile_kernel(LoraArgs p, 
     wait_vmcnt<0>();  // (copies of slices past the last: zeros, but still on their way)
     const int m0 = tm * BM + wm * (BM / WM), n0 = tn * BN + wn * (BN / WN);
     constexpr bool FULL = sizeof(TO) == 4 && std::is_same<T, __bf16>::value;
-    if constexpr (FM * FN >= 32)
-        lora_add_lean<T, FULL>(p, acc, m0, n0);
-    else
-        lora_add<T, FULL>(p, acc, m0, n0);
+    if (KG == 1 || kg == KG - 1) {
+        if constexpr (FM * FN >= 32)
+            lora_add_lean<T, FULL>(p, acc, m0, n0);
+        else
+            lora_add<T, FULL>(p, acc, m0, n0);
+    }
+    if constexpr (KG > 1) {
+        __syncthreads();  // (the rings end here)
+        f32x4_t(*const sum)[FM * FN][64] = (f32x4_t(*)[FM * FN][64])all;
+        if (kg > 0)
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FN; ++j) sum[(kg - 1) * WV + wave][i * FN + j][lane] = acc[i][j];
+        __syncthreads();
+        if (kg > 0) return;
+#pragma unroll
+        for (int x = 0; x < KG - 1; ++x)
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FN; ++j) acc[i][j] += sum[x * WV + wave][i * FN + j][lane];
+    }
     const bool vec = (p.ldo & 3) == 0;
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
@@ -429,10 +457,10 @@ void shrink(const LoraArgs& a, hipStream_t st) {
                        st, a, slots);
 }
 
-template <class T, class TO, int BM, int BN, int S, int WM, int WN>
+template <class T, class TO, int BM, int BN, int S, int WM, int WN, int KG>
 void tiles(const LoraArgs& a, hipStream_t st) {
     const int tm = cdiv_i(a.M, BM), tn = cdiv_i(a.N, BN);
-    hipLaunchKernelGGL((lora_tile_kernel<T, TO, BM, BN, S, WM, WN>), dim3(tm * tn), dim3(64 * WM * WN), 0,
+    hipLaunchKernelGGL((lora_tile_kernel<T, TO, BM, BN, S, WM, WN, KG>), dim3(tm * tn), dim3(64 * WM * WN * KG), 0,
                        st, a, tm, tn);
 }
 
@@ -462,18 +490,19 @@ void product(const LoraArgs& a, int cus, hipStream_t st) {
     }
     if (mb <= 4) return;
     // The largest tile that still gives every compute unit one (128 x 64: three in
-    // four of them).  4096^3: 256 x 256 129 us, 128 x 128 134, 128 x 64 165; 2048 rows
-    // of 4096 x 4096: 112, 71 and 87; 333 rows: 128 x 64 27, 64 x 64 28; 128 rows: 25
-    // and 21.
+    // four of them), as what a unit reads into LDS is what bounds the small ones.
+    // us without adapters, rows of 4096 x 4096: 4096 rows 256 x 256 114, 128 x 128 134,
+    // 128 x 64 165; 2048 rows 112, 71 and 87; 333 rows 128 x 64 25, 64 x 64 31; 128
+    // rows 24 and 17.
     auto count = [&](int64_t bm, int64_t bn) { return (int64_t)cdiv_i(a.M, bm) * cdiv_i(a.N, bn); };
     if (count(256, 256) >= cus)
-        tiles<T, TO, 256, 256, 2, 4, 2>(a, st);
+        tiles<T, TO, 256, 256, 2, 4, 2, 1>(a, st);
     else if (count(128, 128) >= cus)
-        tiles<T, TO, 128, 128, 2, 2, 2>(a, st);
+        tiles<T, TO, 128, 128, 2, 2, 2, 1>(a, st);
     else if (4 * count(128, 64) >= 3 * cus)
-        tiles<T, TO, 128, 64, 3, 4, 2>(a, st);
+        tiles<T, TO, 128, 64, 3, 4, 2, 2>(a, st);
     else
-        tiles<T, TO, 64, 64, 4, 2, 2>(a, st);
+        tiles<T, TO, 64, 64, 4, 4, 2, 2>(a, st);
 }
 
 template <class T>

@@ -174,13 +174,15 @@ __device__ __forceinline__ void turn(float* a, float* b, const float* c, const f
     }
 }
 
-// (token, head) of an item, and of the one GROUPS further: no division a step
+// (token, head) of an item, and of the one `by` further: one division at the start
 struct Item {
-    int t, h;
-    __device__ __forceinline__ Item(int item, int H) : t(item / H), h(item - item / H * H) {}
-    __device__ __forceinline__ void step(int by, int H) {
-        h += by;
-        while (h >= H) h -= H, ++t;
+    int t, h, dt, dh, H;
+    __device__ __forceinline__ Item(int item, int by, int H_)
+        : t(item / H_), h(item - item / H_ * H_), dt(by / H_), dh(by - by / H_ * H_), H(H_) {}
+    __device__ __forceinline__ void step() {
+        t += dt;
+        h += dh;
+        if (h >= H) h -= H, ++t;
     }
 };
 
@@ -236,7 +238,7 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(RopeArgs p) {
                 }
             }
         };
-        Item it(from + group, Hw);
+        Item it(from + group, GROUPS, Hw);
         load(it);
         for (int i0 = from + group; i0 < to; i0 += GROUPS) {
             float y[NU][2 * E];
@@ -244,8 +246,8 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(RopeArgs p) {
             for (int n = 0; n < NU; ++n)
 #pragma unroll
                 for (int i = 0; i < 2 * E; ++i) y[n][i] = x[n][i];
-            const Item now = it;
-            it.step(GROUPS, Hw);
+            const int now_t = it.t, now_h = it.h;
+            it.step();
             if (i0 + GROUPS < to) load(it);
             if (which < 2) {
                 if (p.norm) {
@@ -264,7 +266,7 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(RopeArgs p) {
                 for (int n = 0; n < NU; ++n)
                     if (un[n].turn) {
                         float c[E], sn[E];
-                        const int at = now.t * (p.rot >> 1) + un[n].f;
+                        const int at = now_t * (p.rot >> 1) + un[n].f;
                         lds_floats<E>(&cs[0][at], c);
                         lds_floats<E>(&cs[1][at], sn);
                         turn<E, INTER>(y[n], y[n] + E, c, sn, 1.0f);
@@ -272,7 +274,7 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(RopeArgs p) {
             }
             if (which == 0 || !p.slots) {
                 const HeadView& o = which ? p.ko : p.qo;
-                T* row = (T*)o.p + (int64_t)(t0 + now.t) * o.ts + now.h * o.hs;
+                T* row = (T*)o.p + (int64_t)(t0 + now_t) * o.ts + now_h * o.hs;
 #pragma unroll
                 for (int n = 0; n < NU; ++n)
                     if (un[n].live) {
@@ -281,12 +283,12 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(RopeArgs p) {
                     }
                 continue;
             }
-            const int64_t slot = slot_of[now.t];
+            const int64_t slot = slot_of[now_t];
             if (slot < 0 || slot >= p.num_slots) continue;
             const int page = p.page_shift >= 0 ? (int)slot >> p.page_shift : (int)slot / p.page_size;
             const int at = (int)slot - page * p.page_size;
-            char* row = which == 1 ? (char*)p.kc + page * p.k_page + at * p.k_tok + now.h * p.k_head
-                                   : (char*)p.vc + page * p.v_page + at * p.v_tok + now.h * p.v_head;
+            char* row = which == 1 ? (char*)p.kc + page * p.k_page + at * p.k_tok + now_h * p.k_head
+                                   : (char*)p.vc + page * p.v_page + at * p.v_tok + now_h * p.v_head;
             const float inv = which == 1 ? p.k_inv : p.v_inv;
 #pragma unroll
             for (int n = 0; n < NU; ++n)
@@ -346,8 +348,8 @@ __global__ __launch_bounds__(256) void norm_rope_bwd_kernel(RopeArgs p) {
         const HeadView& dyv = which ? p.dko : p.dqo;
         const HeadView& dxv = which ? p.ko : p.qo;
         if (group >= nt * H) return;
-        Item it(group, H);
-        for (int item = group; item < nt * H; item += GROUPS, it.step(GROUPS, H)) {
+        Item it(group, GROUPS, H);
+        for (int item = group; item < nt * H; item += GROUPS, it.step()) {
             const int t = it.t, h = it.h;
             const T* xr = (const T*)xv.p + (int64_t)(t0 + t) * xv.ts + h * xv.hs;
             const T* dyr = (const T*)dyv.p + (int64_t)(t0 + t) * dyv.ts + h * dyv.hs;

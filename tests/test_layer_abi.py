@@ -163,6 +163,7 @@ def test_attention_refusals():
     for kw in (dict(B=-1), dict(Hq=-8), dict(Hq=7), dict(Hk=0), dict(Hk=3), dict(D=0), dict(most=-1),
                dict(window=-1), dict(ts=-1), dict(out=heads(ts=64)), dict(c=cache(ks=(2048, -8, 64)))):
         assert attn(**kw) == BADSHAPE, kw
+    assert attn(B=65535, Hq=65535, Hk=65535, q=heads(ts=65535 * 64), out=heads(ts=65535 * 64)) == UNSUP_SHAPE
     for kw in (dict(B=65536), dict(D=264), dict(D=60), dict(most=(1 << 30) + 1), dict(ts=1 << 31)):
         assert attn(**kw) == UNSUP_SHAPE, kw
     for kw in (dict(q=None), dict(c=None), dict(c=cache(k=None)), dict(table=None), dict(lengths=None),
