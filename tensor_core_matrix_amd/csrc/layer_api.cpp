@@ -143,8 +143,8 @@ int64_t bwd_workspace(int64_t D) { return int64_t(kRopeBwdGrid) * 2 * D * 4; }
 // The split over the length.  Two ways to deal the work to workgroups of four waves:
 //  * heads == 1: a chunk of one key-value head's keys, its tiles dealt to the
 //    waves.  Chunks of 1024 keys, or fewer (256 at least) where that leaves fewer than
-//    1024 workgroups: 64 sequences of up to 4096 keys take 101 us in chunks of 1024,
-//    102 of 768 and 115 of 2048 (lengths differ: the last chunks idle the device);
+//    1024 workgroups: 64 sequences of up to 4096 keys take 100 us in chunks of 1024,
+//    101 of 768 and 107 of 2048 (lengths differ: the last chunks idle the device);
 //    32 of up to 8192 E4M3 keys 67, and 72 in chunks of 512 (each pays its first
 //    reads' latency).
 //  * heads == 4: the same chunk of four heads, one a wave, so that the

@@ -17,12 +17,19 @@
 // (lane c = l % 16 takes elements c D / 16 .. of each of its 8 keys, so 16 lanes
 // read a whole row), and turned into the 8-keys-of-one-element form by byte
 // permutations within the lane.  Maximum and sum of a head's softmax live in
-// its lanes too: nothing goes through LDS until a workgroup's four waves join.
+// its lanes too.  K is read in whole rows and goes through the wave's own LDS
+// area: read in the operand's pattern of 16 rows x 64 bytes, memory gives 5.2 TB/s
+// to a kernel that does nothing else, in whole rows 6.4.  Nothing waits for another
+// wave until a workgroup's four join at the end.
 //
-// A workgroup takes a chunk of one sequence's keys for one key-value head, its
-// waves 32 keys at a time in turn, the next tile's loads being in flight while
-// one is computed.  With more than one chunk the partial results go to the
-// workspace and attn_join_kernel joins them.
+// A workgroup takes a chunk of a sequence's keys, for one key-value head with its
+// tiles dealt to the four waves or for four heads, one a wave; the next tile's
+// keys and values are on their way while one is computed.  With more than one
+// chunk the partial results go to the workspace and attn_join_kernel joins them.
+//
+// Bound by reads: one sequence of 131001 keys (32 query, 8 key-value heads of 128,
+// fp16) takes 85 us, 6.3 TB/s, and 5 for the join; 64 sequences of up to 4096 keys
+// 97 us, 5.8 TB/s; 32 of up to 8192 in E4M3 62 us, 4.9 TB/s; 200 keys 7.5 us.
 #include <type_traits>
 
 #include "layer_internal.h"
@@ -37,7 +44,6 @@ constexpr float kNegInf = -__builtin_inff();
 template <class T> struct Half16;
 template <> struct Half16<__bf16> {
     typedef bf16x8_t x8;
-    typedef __bf16 x2 __attribute__((ext_vector_type(2)));
     __device__ static __forceinline__ f32x4_t mma(x8 a, x8 b, f32x4_t c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
     }
@@ -48,7 +54,6 @@ template <> struct Half16<__bf16> {
 };
 template <> struct Half16<_Float16> {
     typedef f16x8_t x8;
-    typedef _Float16 x2 __attribute__((ext_vector_type(2)));
     __device__ static __forceinline__ f32x4_t mma(x8 a, x8 b, f32x4_t c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
     }

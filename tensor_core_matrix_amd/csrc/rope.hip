@@ -10,10 +10,12 @@
 // every access is 16 bytes and a head's two halves are contiguous over its
 // lanes; and as what is done once a head and lane -- the sum, the root, the
 // addresses -- is half of the instructions, few lanes a head count as much
-// (8191 tokens of 32 + 8 + 8 heads of 128, E4M3 cache: 43 us, and 77 with E = 4).  The angles of a workgroup's tokens are computed once, by the threads
-// of the workgroup, into LDS: position * inv_freq in 64 bits, reduced to one
-// turn there and only then rounded, so a position near 2^31 is as good as one
-// near 0 and no table has to be read.
+// (8191 tokens of 32 + 8 + 8 heads of 128, E4M3 cache: 42 us, 4.4 TB/s, and 77 with
+// E = 4; backwards 8192 tokens of 32 + 8 heads 52 us, 4.8 TB/s, and 5 for the sums).
+// The angles of a workgroup's tokens are computed once, by its threads, into
+// LDS: position * inv_freq in 64 bits, reduced to one turn there and only then
+// rounded, so a position near 2^31 is as good as one near 0 and no table has to
+// be read.
 #include <type_traits>
 
 #include "layer_internal.h"
@@ -22,9 +24,6 @@
 namespace tcm {
 
 namespace {
-
-template <class T>
-__device__ __forceinline__ float to_f(T x) { return (float)x; }
 
 // E elements at p in one access
 template <int E, class T>
@@ -494,7 +493,7 @@ hipError_t forward(RopeArgs a, bool inter, hipStream_t st) {
         const int H = a.Hq + a.Hk + a.Hv;
         // Tokens a workgroup: as many as leave four workgroups for every compute
         // unit, since each begins with the angles and its first reads (8191 tokens
-        // of 32 + 8 + 8 heads of 128: 47 us, 53 with eight, 60 with 16 and 50 with two);
+        // of 32 + 8 + 8 heads of 128: with eight 6 us more, with 16 13 more, with two 3);
         // with small heads until its items fill its lanes, while every compute unit
         // has a workgroup.
         a.tb = 1;
