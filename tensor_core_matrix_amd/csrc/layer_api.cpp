@@ -20,7 +20,7 @@ constexpr int64_t kMaxK = int64_t(1) << 20;
 constexpr int64_t kMaxLd = int64_t(1) << 21;   // 256 rows of it stay within 32 bits
 constexpr int64_t kMaxRows = int64_t(1) << 30;
 constexpr int64_t kMaxHeads = 65535;
-// a stride (elements) and its product with a count stay far from 64 bits
+// elements; no device memory holds a larger step
 constexpr int64_t kMaxStride = int64_t(1) << 40;
 
 // 16 tokens of a page stay within 32 bits of bytes
@@ -36,11 +36,16 @@ tcm_status launched(hipError_t e) { return e == hipSuccess ? TCM_OK : TCM_ERR_HI
 
 // ---- views ----------------------------------------------------------------------
 
-tcm_status check_heads(const tcm_heads* v) {
+// A stride is not negative, and n steps of it (n >= 0) stay far within 64 bits of bytes.
+bool stride_ok(int64_t n, int64_t stride) {
+    int64_t t;
+    return stride >= 0 && stride <= kMaxStride && !__builtin_mul_overflow(n, stride, &t) &&
+           t < (int64_t(1) << 60);
+}
+
+tcm_status check_heads(const tcm_heads* v, int64_t T, int64_t H) {
     if (!v || !v->ptr) return TCM_ERR_NULL_POINTER;
-    if (v->token_stride < 0 || v->head_stride < 0 || v->token_stride > kMaxStride ||
-        v->head_stride > kMaxStride)
-        return TCM_ERR_INVALID_SHAPE;
+    if (!stride_ok(T, v->token_stride) || !stride_ok(H, v->head_stride)) return TCM_ERR_INVALID_SHAPE;
     if (!aligned16(v->ptr) || v->token_stride % 8 != 0 || v->head_stride % 8 != 0)
         return TCM_ERR_MISALIGNED;
     return TCM_OK;
@@ -48,7 +53,7 @@ tcm_status check_heads(const tcm_heads* v) {
 
 // A view that is written: its tokens and heads lie apart.
 tcm_status check_written(const tcm_heads* v, int64_t T, int64_t H, int64_t D) {
-    tcm_status s = check_heads(v);
+    tcm_status s = check_heads(v, T, H);
     if (s != TCM_OK) return s;
     const int64_t ts = v->token_stride, hs = v->head_stride;
     if (T > 1 && H > 1) {
@@ -70,8 +75,9 @@ tcm_status check_cache(const tcm_cache* c, tcm_dtype dtype, int64_t Hk, int64_t 
     if (c->pages < 0 || c->page_size < 1) return TCM_ERR_INVALID_SHAPE;
     const int64_t st[6] = {c->k_page_stride, c->k_token_stride, c->k_head_stride,
                            c->v_page_stride, c->v_token_stride, c->v_head_stride};
-    for (int64_t s : st)
-        if (s < 0 || s > kMaxStride) return TCM_ERR_INVALID_SHAPE;
+    for (int i = 0; i < 6; ++i)
+        if (!stride_ok(i % 3 == 0 ? c->pages : i % 3 == 1 ? c->page_size : Hk, st[i]))
+            return TCM_ERR_INVALID_SHAPE;
     if (written) {
         // every (page, place, head) its own D elements at least
         for (int i = 0; i < 6; i += 3) {
@@ -285,8 +291,8 @@ tcm_status tcm_qk_norm_rope(const tcm_heads* q, const tcm_heads* k, const tcm_he
     tcm_status s = check_rope(rope, dtype, T, Hq, Hk);
     if (s != TCM_OK || T == 0 || Hq + Hk == 0) return s;
     const int64_t D = rope->head_dim;
-    if (Hq > 0 && ((s = check_heads(q)) != TCM_OK || (s = check_written(q_out, T, Hq, D)) != TCM_OK)) return s;
-    if (Hk > 0 && ((s = check_heads(k)) != TCM_OK || (s = check_written(k_out, T, Hk, D)) != TCM_OK)) return s;
+    if (Hq > 0 && ((s = check_heads(q, T, Hq)) != TCM_OK || (s = check_written(q_out, T, Hq, D)) != TCM_OK)) return s;
+    if (Hk > 0 && ((s = check_heads(k, T, Hk)) != TCM_OK || (s = check_written(k_out, T, Hk, D)) != TCM_OK)) return s;
     DeviceInfo dev;
     if ((s = device_info(&dev)) != TCM_OK) return s;
     RopeArgs a;
@@ -306,8 +312,8 @@ tcm_status tcm_qk_norm_rope_cache(const tcm_heads* q, const tcm_heads* k, const 
     if ((s = check_cache(cache, dtype, Hk, D, true)) != TCM_OK) return s;
     if (T == 0 || Hq + Hk == 0) return TCM_OK;
     if (!slots) return TCM_ERR_NULL_POINTER;
-    if (Hq > 0 && ((s = check_heads(q)) != TCM_OK || (s = check_written(q_out, T, Hq, D)) != TCM_OK)) return s;
-    if (Hk > 0 && ((s = check_heads(k)) != TCM_OK || (s = check_heads(v)) != TCM_OK)) return s;
+    if (Hq > 0 && ((s = check_heads(q, T, Hq)) != TCM_OK || (s = check_written(q_out, T, Hq, D)) != TCM_OK)) return s;
+    if (Hk > 0 && ((s = check_heads(k, T, Hk)) != TCM_OK || (s = check_heads(v, T, Hk)) != TCM_OK)) return s;
     DeviceInfo dev;
     if ((s = device_info(&dev)) != TCM_OK) return s;
     RopeArgs a;
@@ -357,8 +363,8 @@ tcm_status tcm_qk_norm_rope_bwd(const tcm_heads* dq_out, const tcm_heads* dk_out
     for (int i = 0; any && i < 2; ++i) {
         const int64_t H = i ? Hk : Hq;
         if (H == 0) continue;
-        if ((s = check_heads(i ? dk_out : dq_out)) != TCM_OK) return s;
-        if (rope->norm && (s = check_heads(i ? k : q)) != TCM_OK) return s;
+        if ((s = check_heads(i ? dk_out : dq_out, T, H)) != TCM_OK) return s;
+        if (rope->norm && (s = check_heads(i ? k : q, T, H)) != TCM_OK) return s;
         if ((s = check_written(i ? dk : dq, T, H, D)) != TCM_OK) return s;
     }
     if (dw) {
@@ -409,7 +415,7 @@ tcm_status tcm_paged_attention(const tcm_heads* q, const tcm_cache* cache,
     if (cache->dtype == TCM_E4M3 && D % 16 != 0) return TCM_ERR_MISALIGNED;
     if (B == 0 || Hq == 0) return TCM_OK;
     if (!lengths || (table_stride > 0 && !block_table)) return TCM_ERR_NULL_POINTER;
-    if ((s = check_heads(q)) != TCM_OK || (s = check_written(out, B, Hq, D)) != TCM_OK) return s;
+    if ((s = check_heads(q, B, Hq)) != TCM_OK || (s = check_written(out, B, Hq, D)) != TCM_OK) return s;
     // no page, no key
     if (cache->pages == 0) max_len = 0;
     // the first tile of a window begins up to 31 keys before it

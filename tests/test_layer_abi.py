@@ -85,6 +85,7 @@ def test_rope_refusals():
     assert fwd(r=rope(wt=tcm.F32)) in PASSED
     assert fwd(r=rope(wt=tcm.F16, wq=None, wk=None)) in PASSED  # no weight, no type
     assert fwd(r=rope(layout=2)) == BADARG and fwd(r=rope(layout=-1)) == BADARG
+    assert fwd(T=1 << 30, q=heads(ts=1 << 31)) == BADSHAPE and fwd(q=heads(hs=1 << 60)) == BADSHAPE
     for kw in (dict(T=-1), dict(Hq=-1), dict(Hk=-1), dict(r=rope(D=0, rot=0)), dict(r=rope(rot=72)),
                dict(r=rope(rot=31)), dict(r=rope(rot=-2)), dict(q=heads(ts=-512)), dict(qo=heads(ts=256)),
                dict(ko=heads(hs=32)), dict(qo=heads(hs=0))):
@@ -117,7 +118,8 @@ def test_rope_cache_refusals():
     assert into(cache(k=None, v=None, pages=0)) in PASSED
     assert into(cache(dt=tcm.F16)) == UNSUP_DTYPE and into(cache(dt=tcm.F32)) == UNSUP_DTYPE
     for c in (cache(pages=-1), cache(page_size=0), cache(ks=(2048, 128, -64)), cache(ks=(2048, 128, 32)),
-              cache(vs=(2048, 8, 64)), cache(vs=(1 << 41, 128, 64))):
+              cache(vs=(2048, 8, 64)), cache(vs=(1 << 41, 128, 64)),
+              cache(pages=1 << 30, ks=(1 << 40, 128, 64))):
         assert into(c) == BADSHAPE
     assert into(cache(page_size=(1 << 20) + 1)) == UNSUP_SHAPE
     for kw in (dict(c=None), dict(c=cache(k=None)), dict(c=cache(v=None)), dict(slots=None), dict(v=None)):
