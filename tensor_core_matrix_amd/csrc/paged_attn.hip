@@ -33,6 +33,7 @@
 #include <type_traits>
 
 #include "layer_internal.h"
+#include "paged_rows.h"
 #include "tcm_device.h"
 
 namespace tcm {
@@ -124,7 +125,9 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : DP == 128 && E4M3 && ALIGNED ?
     constexpr int ES = E4M3 ? 1 : 2;
     constexpr int STEPS = DP / 32;          // products of 32 over the head
     constexpr int VE = DP / 16;             // elements of a value row a lane holds
-    constexpr int VW = VE * ES / 4;         // words of a lane's piece of a value row
+    constexpr int VW = VE * ES / 4;         // words of a lane's piece of a value row,
+    constexpr int VB = value_load(DP, ES);  // bytes of one load of it
+    constexpr int VL = VW * 4 / VB;         // and its loads
     constexpr int KB = DP * ES;             // bytes of a key
     constexpr int KL = KB / 16;             // lanes that read a key,
     constexpr int KN = 64 / KL;             // keys of one read
@@ -218,18 +221,20 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : DP == 128 && E4M3 && ALIGNED ?
     auto swz = [](int key) { return (key >> SH) & ((KL < 16 ? KL : 16) - 1); };
     char* const ka = lds + wave * KA;
     const int kc = lane % KL, kr = lane / KL;
-    // D < DP: pieces of a key past its end are zeros that nothing overwrites; lanes
+    // D < DP: pieces of a key past its end are zeros that nothing overwrites; loads
     // past the end of a value row read its beginning for elements nobody stores
-    const bool kin = kc * (16 / ES) < p.D;
+    const bool kin = key_piece_in(kc, p.D, ES);
     if (!kin)
 #pragma unroll
         for (int i = 0; i < KI; ++i)
             *(i32x4_t*)(ka + (i * KN + kr) * KB + (kc ^ swz(i * KN + kr)) * 16) = (i32x4_t){};
-    const int vc = r16 * VE < p.D ? r16 * VE * ES : 0;
+    int vc[VL];
+#pragma unroll
+    for (int i = 0; i < VL; ++i) vc[i] = value_at(r16, i, p.D, DP, ES);
     // ALIGNED: a lane's offsets from the first of 16 keys (16 token strides are
     // less than 2^31 bytes)
     const uint32_t koff = (uint32_t)kr * (uint32_t)p.k_tok + kc * 16;
-    const uint32_t voff = (uint32_t)(4 * g4) * (uint32_t)p.v_tok + vc;
+    const uint32_t voff = (uint32_t)(4 * g4) * (uint32_t)p.v_tok;
     const char* const kh = p.kc + hk * p.k_head;
     const char* const vh = p.vc + hk * p.v_head;
     // the keys of inner positions 0..7 of this lane in the second product
@@ -262,13 +267,18 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : DP == 128 && E4M3 && ALIGNED ?
 #pragma unroll
             for (int h = 0; h < 2; ++h) vb[h] = vh + max(w.page[h], 0) * p.v_page + w.at[h] * p.v_tok;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) load_words<VW>(vb[j >> 2] + (j & 3) * p.v_tok + voff, t.v[j]);
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int i = 0; i < VL; ++i)
+                    load_words<VB / 4>(vb[j >> 2] + (j & 3) * p.v_tok + (voff + vc[i]), t.v[j] + i * (VB / 4));
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                load_words<VW>(vh + max(__shfl(w.page[0], vkey(j)), 0) * p.v_page +
-                                   __shfl(w.at[0], vkey(j)) * p.v_tok + vc,
-                               t.v[j]);
+            for (int j = 0; j < 8; ++j) {
+                const char* row = vh + max(__shfl(w.page[0], vkey(j)), 0) * p.v_page +
+                                  __shfl(w.at[0], vkey(j)) * p.v_tok;
+#pragma unroll
+                for (int i = 0; i < VL; ++i) load_words<VB / 4>(row + vc[i], t.v[j] + i * (VB / 4));
+            }
         }
     };
 
@@ -564,9 +574,11 @@ hipError_t run(const AttnArgs& a, hipStream_t st) {
 
 template <class T>
 hipError_t by_dim(const AttnArgs& a, bool e4m3, hipStream_t st) {
-    if (a.D <= 64) return e4m3 ? run<T, 64, true>(a, st) : run<T, 64, false>(a, st);
-    if (a.D <= 128) return e4m3 ? run<T, 128, true>(a, st) : run<T, 128, false>(a, st);
-    return e4m3 ? run<T, 256, true>(a, st) : run<T, 256, false>(a, st);
+    switch (head_instance(a.D)) {
+    case 64: return e4m3 ? run<T, 64, true>(a, st) : run<T, 64, false>(a, st);
+    case 128: return e4m3 ? run<T, 128, true>(a, st) : run<T, 128, false>(a, st);
+    default: return e4m3 ? run<T, 256, true>(a, st) : run<T, 256, false>(a, st);
+    }
 }
 
 }  // namespace
