@@ -42,8 +42,13 @@ namespace {
 
 constexpr float kNegInf = -__builtin_inff();
 
+// kLift: what probabilities are multiplied by on their way into the second product, whose
+// result is divided by it where the waves' parts meet.  They are at most 1, and fp16 ends at
+// 2^-24: as they are, thousands of keys 2^-25 below the largest would vanish from the
+// product and count in the sum.  bf16 has fp32's exponents.
 template <class T> struct Half16;
 template <> struct Half16<__bf16> {
+    static constexpr float kLift = 1.0f;
     typedef bf16x8_t x8;
     __device__ static __forceinline__ f32x4_t mma(x8 a, x8 b, f32x4_t c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
@@ -54,6 +59,7 @@ template <> struct Half16<__bf16> {
     }
 };
 template <> struct Half16<_Float16> {
+    static constexpr float kLift = 32768.0f;
     typedef f16x8_t x8;
     __device__ static __forceinline__ f32x4_t mma(x8 a, x8 b, f32x4_t c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
@@ -376,7 +382,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : DP == 128 && E4M3 && ALIGNED ?
         for (int j = 0; j < 8; ++j) {
             const float e = __builtin_amdgcn_exp2f(x[j] - m0);
             sum += e;
-            pf[j] = (T)e;
+            pf[j] = (T)(e * H::kLift);
         }
         // 8 keys x VE elements -> VE operands of 8 keys
 #pragma unroll
@@ -455,7 +461,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : DP == 128 && E4M3 && ALIGNED ?
         for (int w = hh + p.heads; w < 4; w += p.heads) t = fmaxf(t, lm_[w][q]);
         return t;
     };
-    const float f = mx == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mx - head_top(hw, r16));
+    const float f = mx == kNegInf ? 0.0f : 1.0f / H::kLift * __builtin_amdgcn_exp2f(mx - head_top(hw, r16));
     // lane l holds elements (4 g + i) VE + m of head l % 16
 #pragma unroll
     for (int i = 0; i < 4; ++i)
