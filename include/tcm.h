@@ -473,8 +473,9 @@ tcm_status tcm_qk_norm_rope_bwd_workspace(int64_t head_dim, int64_t* bytes);
  * A sequence without keys gives out = 0 and lse = -infinity.  Cache memory
  * that holds no attended key is not used and may hold anything.
  * dtype (q, out) TCM_F16 or TCM_BF16, the cache's dtype the same or TCM_E4M3.  Scores,
- * softmax and sums in fp32; the probabilities enter the second product rounded
- * to dtype.  D a multiple of 8 (16 for TCM_E4M3 caches), at most 256; Hq a multiple of
+ * softmax and sums in fp32; the probabilities enter the second product as the
+ * sum of two values of dtype (16 bits of them for TCM_BF16, 22 for TCM_F16, of
+ * which those 2^-40 of a row's largest are the last).  D a multiple of 8 (16 for TCM_E4M3 caches), at most 256; Hq a multiple of
  * Hk; B and Hq at most 65535.
  */
 tcm_status tcm_paged_attention(const tcm_heads* q, const tcm_cache* cache,

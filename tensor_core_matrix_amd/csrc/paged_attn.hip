@@ -16,8 +16,12 @@
 // input without leaving its lane.  V is read 8 keys x D / 16 elements a lane
 // (lane c = l % 16 takes elements c D / 16 .. of each of its 8 keys, so 16 lanes
 // read a whole row), and turned into the 8-keys-of-one-element form by byte
-// permutations within the lane.  Maximum and sum of a head's softmax live in
-// its lanes too.  K is read in whole rows and goes through the wave's own LDS
+// permutations within the lane.  A probability is rounded to the type's 8 or 11 bits
+// there, and what that leaves is rounded and multiplied too: 16 or 22 bits together, so
+// that the result's error is its own rounding (one product in bf16: a third more).  The
+// second products cost 1 to 2 % (64 sequences of up to 4096 keys 102.5 us, and 100.8
+// without).
+// Maximum and sum of a head's softmax live in its lanes too.  K is read in whole rows and goes through the wave's own LDS
 // area: read in the operand's pattern of 16 rows x 64 bytes, memory gives 5.2 TB/s
 // to a kernel that does nothing else, in whole rows 6.4.  Nothing waits for another
 // wave until a workgroup's four join at the end.
@@ -293,8 +297,9 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : DP == 128 && E4M3 && ALIGNED ?
     for (int m = 0; m < VE; ++m) o[m] = (f32x4_t){};
     float mx = kNegInf, sum = 0.0f;
 
-    // (`next` asks for the next tile's keys, once the registers of these are free)
-    auto compute = [&](Keys& kt, Values& t, const Where& w, int key0, auto&& next) {
+    // (`next` asks for the next tile's keys, once the registers of these are free;
+    // `upper`: what a probability's upper part is rounded from)
+    auto compute = [&](Keys& kt, Values& t, const Where& w, int key0, float upper, auto&& next) {
         // a tile with unusable keys: their scores become -infinity and, since a
         // probability of 0 times what lies in such a place may be NaN, their
         // values 0
@@ -377,12 +382,13 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : DP == 128 && E4M3 && ALIGNED ?
                 for (int i = 0; i < 4; ++i) o[m][i] *= f;
         }
         const float m0 = mx == kNegInf ? 0.0f : mx;
-        x8 pf;
+        x8 pf, pr;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float e = __builtin_amdgcn_exp2f(x[j] - m0);
             sum += e;
-            pf[j] = (T)(e * H::kLift);
+            pf[j] = (T)(e * upper);
+            pr[j] = (T)(e * H::kLift - (float)pf[j]);
         }
         // 8 keys x VE elements -> VE operands of 8 keys
 #pragma unroll
@@ -401,8 +407,11 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : DP == 128 && E4M3 && ALIGNED ?
                 lo[jj] = __builtin_amdgcn_perm(v1, v0, 0x05040100);
                 hi[jj] = __builtin_amdgcn_perm(v1, v0, 0x07060302);
             }
-            o[m] = H::mma(__builtin_bit_cast(x8, *(i32x4_t*)lo), pf, o[m]);
-            o[m + 1] = H::mma(__builtin_bit_cast(x8, *(i32x4_t*)hi), pf, o[m + 1]);
+            const x8 v0 = __builtin_bit_cast(x8, *(i32x4_t*)lo), v1 = __builtin_bit_cast(x8, *(i32x4_t*)hi);
+            o[m] = H::mma(v0, pf, o[m]);
+            o[m + 1] = H::mma(v1, pf, o[m + 1]);
+            o[m] = H::mma(v0, pr, o[m]);
+            o[m + 1] = H::mma(v1, pr, o[m + 1]);
         }
     };
 
@@ -411,36 +420,55 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : DP == 128 && E4M3 && ALIGNED ?
     // keys are free as soon as they are in LDS), and its successor's pages are
     // looked up (asked for before those loads, so that waiting for them is no wait
     // for the loads).
-    int key = start + 32 * kw;
-    if (key < end) {
-        Keys kt;
-        Values va, vb;
-        Where wa = look(key), wb = look(key + round), wc;
-        settle(wa);
-        load_keys(kt, wa);
-        load_values(va, wa);
-        for (;;) {
-            settle(wb);
-            wc = look(key + 2 * round);
-            bool more = key + round < end;
-            if (more) load_values(vb, wb);
-            compute(kt, va, wa, key, [&] {
-                if (more) load_keys(kt, wb);
-            });
-            if (!more) break;
-            key += round;
-            settle(wc);
-            wa = look(key + 2 * round);
-            more = key + round < end;
-            if (more) load_values(va, wc);
-            compute(kt, vb, wb, key, [&] {
-                if (more) load_keys(kt, wc);
-            });
-            if (!more) break;
-            key += round;
-            wb = wa;
-            wa = wc;
+    // An infinite value times a lower part that is zero, or has the other sign, is NaN where
+    // the sum is infinite: a wave that ends with one (E4M3 has no infinities) goes over its
+    // keys again, for the heads that have one with parts that are both half of a
+    // probability, and one sign; the others come to the same bits.
+    for (float upper = H::kLift;;) {
+        int key = start + 32 * kw;
+        if (key < end) {
+            Keys kt;
+            Values va, vb;
+            Where wa = look(key), wb = look(key + round), wc;
+            settle(wa);
+            load_keys(kt, wa);
+            load_values(va, wa);
+            for (;;) {
+                settle(wb);
+                wc = look(key + 2 * round);
+                bool more = key + round < end;
+                if (more) load_values(vb, wb);
+                compute(kt, va, wa, key, upper, [&] {
+                    if (more) load_keys(kt, wb);
+                });
+                if (!more) break;
+                key += round;
+                settle(wc);
+                wa = look(key + 2 * round);
+                more = key + round < end;
+                if (more) load_values(va, wc);
+                compute(kt, vb, wb, key, upper, [&] {
+                    if (more) load_keys(kt, wc);
+                });
+                if (!more) break;
+                key += round;
+                wb = wa;
+                wa = wc;
+            }
         }
+        if (E4M3 || __any(upper != H::kLift)) break;
+        bool nan = false;
+#pragma unroll
+        for (int m = 0; m < VE; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) nan |= o[m][i] != o[m][i];
+        const uint64_t in = __ballot(nan);
+        if (!in) break;
+        if (in >> r16 & 0x0001000100010001u) upper = 0.5f * H::kLift;
+#pragma unroll
+        for (int m = 0; m < VE; ++m) o[m] = (f32x4_t){};
+        mx = kNegInf;
+        sum = 0.0f;
     }
 
     // ---- the four waves' parts ------------------------------------------------
