@@ -337,9 +337,9 @@ tcm_status tcm_plan_gemm(int64_t batch, int64_t M, int64_t N, int64_t K, tcm_dty
  * dtype TCM_F16 or TCM_BF16 (X, W, A, B); out_dtype the same or TCM_F32.  All
  * sums are fp32 and the result is rounded once.  With more than 64 rows the
  * inner product X[i] . A_a^T (times s_a) enters the second product as a sum of
- * two 16-bit values, which hold its upper 16 bits (TCM_F16: 22; fp32 outputs of
- * TCM_BF16: three, 24 bits); for TCM_F16 its magnitude must then stay below
- * 65520, past which the row's output is infinite or NaN.  A row's output
+ * two 16-bit values, which hold 16 bits of it (TCM_F16: 22 bits of the largest
+ * of 16 consecutive ranks; fp32 outputs of TCM_BF16: three values, 24 bits),
+ * whatever its size.  A row's output
  * depends on its own adapter only: values that are not finite in one adapter
  * do not reach the rows of another.
  * R a multiple of 8, at most 128; K a multiple of 8 (TCM_ERR_MISALIGNED

@@ -11,6 +11,10 @@
 // costs nothing below rank 32 and little above it.)  For fp32 outputs of bf16
 // operands a second product adds what the two halves leave.
 //
+// A row's 16 values are multiplied by a power of two first, which brings the largest of
+// them into [2^14, 2^15), and the product by its inverse: fp16 ends at 65504, and below
+// 2^-14 it has fewer digits.  So each step's product is taken by itself and added in fp32.
+//
 // A block is multiplied once for every adapter that its 16 rows name, and only
 // the rows that name it take the result: a row never sees another adapter's
 // values, not even as 0 times infinity.
@@ -72,30 +76,42 @@ __device__ __forceinline__ f32x8 lora_t8(const LoraArgs& p, int m, int r) {
 
 // The t operand of ranks r0 .. r0 + 15 of the block's rows: lane l holds row
 // l % 16, ranks r0 + 8 (g % 2) + 0..7 of the upper (g < 2) or lower half, g = l / 16.
-// Lanes whose row is not `mine` get zeros (their t was never written).  REST: what
-// the two halves leave, and zeros beside it.
-template <class T, bool REST = false>
-__device__ __forceinline__ typename LoraMma<T>::x8 lora_t(const LoraArgs& p, int m, int r0, int g4,
-                                                          bool mine) {
-    typedef typename LoraMma<T>::x8 x8;
+// Lanes whose row is not `mine` get zeros (their t was never written).  rest: what
+// the two halves leave, and zeros beside it (FULL).  up: what the row's products are
+// multiplied by.
+template <class T> struct LoraT {
+    typename LoraMma<T>::x8 f, rest;
+    float up;
+};
+template <class T, bool FULL>
+__device__ __forceinline__ LoraT<T> lora_t(const LoraArgs& p, int m, int r0, int g4, bool mine) {
     const int r = r0 + 8 * (g4 & 1);
-    x8 f = {};
-    if (mine && r < p.R) {
-        const f32x8 t = lora_t8(p, m, r);
+    f32x8 t = {};
+    if (mine && r < p.R) t = lora_t8(p, m, r);
+    float top = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const T hi = convert_out<T>(t[j]);
-            const float rest = t[j] - (float)hi;
-            // (where the upper half is infinite or NaN it says all)
-            const T lo = rest == rest ? convert_out<T>(rest) : (T)0.0f;
+    for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(t[j]));
+    const auto both = __builtin_amdgcn_permlane16_swap(__float_as_uint(top), __float_as_uint(top), false, false);
+    top = fmaxf(__uint_as_float(both[0]), __uint_as_float(both[1]));
+    // 2^k and 2^-k, both normal; an infinite value counts as the largest finite one
+    const int k = min(14 + 127 - (int)(__float_as_uint(top) >> 23), 126);
+    const float down = __uint_as_float((uint32_t)(127 + k) << 23);
+    LoraT<T> o;
+    o.up = __uint_as_float((uint32_t)(127 - k) << 23);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float x = t[j] * down;
+        const T hi = convert_out<T>(x);
+        const float rest = x - (float)hi;
+        // (an infinite or NaN upper half, which is t itself, says all)
+        const T lo = rest == rest ? convert_out<T>(rest) : (T)0.0f;
+        o.f[j] = g4 < 2 ? hi : lo;
+        if constexpr (FULL) {
             const float last = rest - (float)lo;
-            if constexpr (REST)
-                f[j] = g4 < 2 && last == last ? convert_out<T>(last) : (T)0.0f;
-            else
-                f[j] = g4 < 2 ? hi : lo;
+            o.rest[j] = g4 < 2 && last == last ? convert_out<T>(last) : (T)0.0f;
         }
     }
-    return f;
+    return o;
 }
 
 // The B operand: row n of B_a, the same ranks; zeros from the adapter's rank on.
@@ -139,21 +155,19 @@ __device__ __forceinline__ void lora_add(const LoraArgs& p, f32x4_t (&acc)[NI][N
     if (__ballot(!same) == 0) {
         const int rank = lora_rank(p, one);
         for (int r0 = 0; r0 < rank; r0 += 16) {
-            x8 b[NJ], t[NI];
+            x8 b[NJ];
+            LoraT<T> t[NI];
 #pragma unroll
             for (int j = 0; j < NJ; ++j) b[j] = lora_b<T>(p, one, rank, n0 + 16 * j + r16, r0, g4);
 #pragma unroll
-            for (int i = 0; i < NI; ++i) t[i] = lora_t<T>(p, m0 + 16 * i + r16, r0, g4, true);
+            for (int i = 0; i < NI; ++i) t[i] = lora_t<T, FULL>(p, m0 + 16 * i + r16, r0, g4, true);
 #pragma unroll
             for (int i = 0; i < NI; ++i)
 #pragma unroll
-                for (int j = 0; j < NJ; ++j) acc[i][j] = O::mma(b[j], t[i], acc[i][j]);
-            if constexpr (FULL)
-#pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    const x8 u = lora_t<T, true>(p, m0 + 16 * i + r16, r0, g4, true);
-#pragma unroll
-                    for (int j = 0; j < NJ; ++j) acc[i][j] = O::mma(b[j], u, acc[i][j]);
+                for (int j = 0; j < NJ; ++j) {
+                    f32x4_t d = O::mma(b[j], t[i].f, (f32x4_t){});
+                    if constexpr (FULL) d = O::mma(b[j], t[i].rest, d);
+                    acc[i][j] += d * t[i].up;
                 }
         }
         return;
@@ -171,25 +185,19 @@ __device__ __forceinline__ void lora_add(const LoraArgs& p, f32x4_t (&acc)[NI][N
                 const int a = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
                 left &= ~(uint32_t)__ballot(id == a);
                 const int rank = lora_rank(p, a);
-                f32x4_t d[NJ];
-#pragma unroll
-                for (int j = 0; j < NJ; ++j) d[j] = (f32x4_t){};
                 for (int r0 = 0; r0 < rank; r0 += 16) {
                     x8 b[NJ];
 #pragma unroll
                     for (int j = 0; j < NJ; ++j) b[j] = lora_b<T>(p, a, rank, n0 + 16 * j + r16, r0, g4);
-                    const x8 t = lora_t<T>(p, m, r0, g4, id == a);
+                    const LoraT<T> t = lora_t<T, FULL>(p, m, r0, g4, id == a);
 #pragma unroll
-                    for (int j = 0; j < NJ; ++j) d[j] = O::mma(b[j], t, d[j]);
-                    if constexpr (FULL) {
-                        const x8 u = lora_t<T, true>(p, m, r0, g4, id == a);
+                    for (int j = 0; j < NJ; ++j) {
+                        f32x4_t d = O::mma(b[j], t.f, (f32x4_t){});
+                        if constexpr (FULL) d = O::mma(b[j], t.rest, d);
 #pragma unroll
-                        for (int j = 0; j < NJ; ++j) d[j] = O::mma(b[j], u, d[j]);
+                        for (int e = 0; e < 4; ++e) acc[i][j][e] += id == a ? d[e] * t.up : 0.0f;
                     }
                 }
-                if (id == a)
-#pragma unroll
-                    for (int j = 0; j < NJ; ++j) acc[i][j] += d[j];
             }
             continue;
         }
@@ -233,9 +241,7 @@ __device__ __forceinline__ void lora_add_lean(const LoraArgs& p, f32x4_t (&acc)[
             left &= ~(uint32_t)__ballot(id == a);
             const int rank = lora_rank(p, a);
             for (int r0 = 0; r0 < rank; r0 += 16) {
-                const x8 t = lora_t<T>(p, m0 + 16 * i + r16, r0, g4, id == a);
-                x8 u;
-                if constexpr (FULL) u = lora_t<T, true>(p, m0 + 16 * i + r16, r0, g4, id == a);
+                const LoraT<T> t = lora_t<T, FULL>(p, m0 + 16 * i + r16, r0, g4, id == a);
 #pragma unroll
                 for (int j0 = 0; j0 < NJ; j0 += 4) {
                     x8 b[4];
@@ -243,10 +249,10 @@ __device__ __forceinline__ void lora_add_lean(const LoraArgs& p, f32x4_t (&acc)[
                     for (int j = 0; j < 4; ++j) b[j] = lora_b<T>(p, a, rank, n0 + 16 * (j0 + j) + r16, r0, g4);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        f32x4_t d = O::mma(b[j], t, (f32x4_t){});
-                        if constexpr (FULL) d = O::mma(b[j], u, d);
+                        f32x4_t d = O::mma(b[j], t.f, (f32x4_t){});
+                        if constexpr (FULL) d = O::mma(b[j], t.rest, d);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[i][j0 + j][e] += id == a ? d[e] : 0.0f;
+                        for (int e = 0; e < 4; ++e) acc[i][j0 + j][e] += id == a ? d[e] * t.up : 0.0f;
                     }
                     __builtin_amdgcn_sched_barrier(0);
                 }
