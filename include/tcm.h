@@ -351,6 +351,7 @@ tcm_status tcm_lora_gemm_tn(const void* X, int64_t ldx, const void* W, const voi
                             const float* scales, void* Out, int64_t ldo, int64_t M, int64_t N,
                             int64_t K, int64_t L, int64_t R, tcm_dtype dtype, tcm_dtype out_dtype,
                             void* workspace, int64_t workspace_bytes, void* stream);
+/* (enough also for smaller M, K and R) */
 tcm_status tcm_lora_workspace(int64_t M, int64_t K, int64_t R, int64_t* bytes);
 
 /* A view of T tokens x H heads x D elements, the D elements of a head

@@ -219,6 +219,22 @@ int64_t lora_parts(int64_t M, int64_t K, int64_t* kpart) {
     return n > 0 ? n : 1;
 }
 
+// No lora_parts() of at most M rows and K values times its rows is more.  The parts that
+// rows and K allow fall with the rows, in steps whose last rows are the most of each (15
+// rows of up to eight parts, then 16 for every sixteenth of 1024 / n), and grow with K.
+int64_t lora_most_rows(int64_t M, int64_t K) {
+    auto rows = [&](int64_t last, int64_t n) {
+        const int64_t fit = K / 1024 > 1 ? K / 1024 : 1;
+        return (M < last ? M : last) * (n < fit ? n : fit);
+    };
+    int64_t most = rows(15, 8);
+    for (int64_t n = 1; n <= 4; ++n) {
+        const int64_t r = n > 1 ? rows(16 * (1024 / n), n) : M;
+        if (r > most) most = r;
+    }
+    return most;
+}
+
 tcm_status check_lora_sizes(int64_t M, int64_t K, int64_t R) {
     if (M < 0 || K < 0 || R < 0) return TCM_ERR_INVALID_SHAPE;
     if (M > kMaxRows || K > kMaxK || R > kLoraMaxRank) return TCM_ERR_UNSUPPORTED_SHAPE;
@@ -233,8 +249,7 @@ tcm_status tcm_lora_workspace(int64_t M, int64_t K, int64_t R, int64_t* bytes) {
     if (!bytes) return TCM_ERR_NULL_POINTER;
     tcm_status s = check_lora_sizes(M, K, R);
     if (s != TCM_OK) return s;
-    int64_t kpart;
-    *bytes = lora_parts(M, K, &kpart) * M * R * 4;
+    *bytes = lora_most_rows(M, K) * R * 4;
     return TCM_OK;
 }
 

@@ -136,7 +136,7 @@ def _run(dev, f, *args):
 
 
 def lora_workspace(M, K, R):
-    """Bytes of workspace of lora_gemm_tn."""
+    """Bytes of workspace of lora_gemm_tn, enough also for fewer rows, a smaller K or R."""
     return _bytes(lib().tcm_lora_workspace, M, K, R)
 
 
