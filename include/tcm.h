@@ -485,7 +485,7 @@ tcm_status tcm_paged_attention(const tcm_heads* q, const tcm_cache* cache,
                                float* lse, int64_t B, int64_t Hq, int64_t Hk, int64_t D,
                                float scale, int64_t window, tcm_dtype dtype, void* workspace,
                                int64_t workspace_bytes, void* stream);
-/* (enough also for smaller max_len and for every window) */
+/* (enough also for smaller B and max_len and for every window) */
 tcm_status tcm_paged_attention_workspace(int64_t B, int64_t Hq, int64_t Hk, int64_t D,
                                          int64_t max_len, int64_t* bytes);
 

@@ -179,16 +179,23 @@ Split split_of(int64_t B, int64_t Hq, int64_t Hk, int64_t span) {
     if (s.n < 1) s.n = 1;
     return s;
 }
-// No split_of() with these sizes and at most this span has more chunks.
-int64_t most_splits(int64_t B, int64_t Hq, int64_t Hk, int64_t span) {
-    int64_t n = cdiv(1024, split_units(B, Hq, Hk));
-    if (n < cdiv(span, kChunk)) n = cdiv(span, kChunk);
-    if (n > cdiv(span, kMinChunk)) n = cdiv(span, kMinChunk);
-    return n < kAttnMaxSplits ? n : kAttnMaxSplits;
+// No split_of() of at most B sequences and this span has more chunks over all of them
+// (0: none has more than one a sequence).  Either the chunks are the longest, or they
+// are cut for 1024 workgroups over `units` a sequence: ceil(x / b) chunks of b
+// sequences, x = ceil(1024 / units), are fewer than x + b, for b < x.
+int64_t most_chunks(int64_t B, int64_t Hq, int64_t Hk, int64_t span) {
+    const int64_t longest = cdiv(span, kChunk), shortest = cdiv(span, kMinChunk);
+    const int64_t lo = longest < kAttnMaxSplits ? longest : kAttnMaxSplits;
+    const int64_t hi = shortest < kAttnMaxSplits ? shortest : kAttnMaxSplits;
+    const int64_t x = cdiv(1024, split_units(1, Hq, Hk));
+    int64_t cut = x + (B < x ? B : x) - 1;
+    if (cut > B * hi) cut = B * hi;
+    if (hi <= 1) cut = 0;
+    const int64_t whole = lo > 1 ? B * lo : 0;
+    return cut > whole ? cut : whole;
 }
-int64_t attn_workspace(int64_t B, int64_t Hq, int64_t D, int64_t n) {
-    return n > 1 ? B * Hq * n * (D + 2) * 4 : 0;
-}
+// of so many chunks over all sequences
+int64_t attn_workspace(int64_t chunks, int64_t Hq, int64_t D) { return chunks * Hq * (D + 2) * 4; }
 
 tcm_status check_attn_sizes(int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t max_len) {
     if (B < 0 || Hq < 0 || Hk < 0 || D < 1 || max_len < 0) return TCM_ERR_INVALID_SHAPE;
@@ -410,8 +417,7 @@ tcm_status tcm_paged_attention_workspace(int64_t B, int64_t Hq, int64_t Hk, int6
     if (!bytes) return TCM_ERR_NULL_POINTER;
     tcm_status s = check_attn_sizes(B, Hq, Hk, D, max_len);
     if (s != TCM_OK) return s;
-    const int64_t n = Hk > 0 ? most_splits(B, Hq, Hk, max_len) : 1;
-    *bytes = attn_workspace(B, Hq, D, n);
+    *bytes = Hk > 0 ? attn_workspace(most_chunks(B, Hq, Hk, max_len), Hq, D) : 0;
     return TCM_OK;
 }
 
@@ -440,7 +446,7 @@ tcm_status tcm_paged_attention(const tcm_heads* q, const tcm_cache* cache,
     if (sp.n > 1) {
         if (!workspace) return TCM_ERR_NULL_POINTER;
         if (!aligned16(workspace)) return TCM_ERR_MISALIGNED;
-        if (workspace_bytes < attn_workspace(B, Hq, D, sp.n)) return TCM_ERR_WORKSPACE;
+        if (workspace_bytes < attn_workspace(B * sp.n, Hq, D)) return TCM_ERR_WORKSPACE;
     }
     DeviceInfo dev;
     if ((s = device_info(&dev)) != TCM_OK) return s;

@@ -270,7 +270,8 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, positions, inv_freq, wq=None, wk=None
 
 
 def paged_attention_workspace(B, Hq, Hk, D, max_len):
-    """Bytes of workspace of paged_attention (for lengths up to max_len)."""
+    """Bytes of workspace of paged_attention, for at most B sequences of lengths up to
+    max_len and every window."""
     return _bytes(lib().tcm_paged_attention_workspace, B, Hq, Hk, D, max_len)
 
 
