@@ -396,9 +396,10 @@ typedef enum tcm_rope_layout {
  * and the pairs (n1, n2) of the first rot_dim elements turned by the angle
  * t = position * inv_freq[j]:
  *   y1 = factor (n1 cos t - n2 sin t),  y2 = factor (n2 cos t + n1 sin t);
- * the other D - rot_dim elements are n.  The angle is computed and reduced in 64
- * bits, so it is exact to 1e-7 for every int32 position; tables are not needed,
- * and a scaling for long contexts is a choice of inv_freq and factor.
+ * the other D - rot_dim elements are n.  The angle is computed and reduced in two
+ * times 64 bits and rounded once to fp32, so it is exact to 1e-7 for every int32
+ * position; tables are not needed, and a scaling for long contexts is a choice of
+ * inv_freq and factor.
  *   head_dim  D, a multiple of 8, at most 256 (TCM_ERR_UNSUPPORTED_SHAPE)
  *   rot_dim   even, 0 .. D (TCM_ERR_INVALID_SHAPE)
  *   positions T int32;  inv_freq  rot_dim / 2 doubles (both NULL if rot_dim == 0)
