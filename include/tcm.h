@@ -434,8 +434,8 @@ tcm_status tcm_qk_norm_rope(const tcm_heads* q, const tcm_heads* k, const tcm_he
  * token t goes to slot slots[t] = page * page_size + place in the page.  A slot
  * outside 0 .. pages * page_size - 1 (-1 by custom) writes nothing to the cache;
  * its query is computed all the same.  No two tokens may have the same slot.
- * TCM_E4M3 caches take x / scale, clamped to +-448 and rounded to nearest
- * even (NaN stays NaN).
+ * TCM_E4M3 caches take the fp32 quotient x / scale, clamped to +-448 and rounded
+ * to nearest even (NaN stays NaN); scales are finite and not zero.
  */
 tcm_status tcm_qk_norm_rope_cache(const tcm_heads* q, const tcm_heads* k, const tcm_heads* v,
                                   const tcm_heads* q_out, const tcm_cache* cache,

@@ -142,6 +142,16 @@ void fill_rope(RopeArgs* a, const tcm_rope* r, int64_t T, int64_t Hq, int64_t Hk
     a->inv_d = 1.0f / (float)r->head_dim;
 }
 
+E4m3Scale scale_parts(float scale) {
+    E4m3Scale s;
+    int e = 0;
+    s.m = frexpf(scale, &e);
+    s.inv = 1.0f / s.m;
+    s.top = 448.0f * fabsf(s.m);
+    s.e = e;
+    return s;
+}
+
 int64_t bwd_workspace(int64_t D) { return int64_t(kRopeBwdGrid) * 2 * D * 4; }
 
 // ---- paged attention ----------------------------------------------------------------
@@ -357,8 +367,8 @@ tcm_status tcm_qk_norm_rope_cache(const tcm_heads* q, const tcm_heads* k, const 
     a.v_page = cache->v_page_stride * es;
     a.v_tok = cache->v_token_stride * es;
     a.v_head = cache->v_head_stride * es;
-    a.k_inv = 1.0f / cache->k_scale;
-    a.v_inv = 1.0f / cache->v_scale;
+    a.k_scale = scale_parts(cache->k_scale);
+    a.v_scale = scale_parts(cache->v_scale);
     return launched(launch_norm_rope(a, (int32_t)dtype, (int32_t)rope->layout, (hipStream_t)stream));
 }
 

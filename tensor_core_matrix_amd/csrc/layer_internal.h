@@ -18,6 +18,12 @@ struct HeadView {
     int64_t ts, hs;
 };
 
+// A scale 2^e m, 1/2 <= |m| < 1, with 1 / m and 448 |m|.
+struct E4m3Scale {
+    float m, inv, top;
+    int32_t e;
+};
+
 struct RopeArgs {
     HeadView q, k, v;    // inputs (backward: the inputs of the forward pass)
     HeadView qo, ko;     // outputs (backward: gradients of the inputs)
@@ -41,7 +47,7 @@ struct RopeArgs {
     int64_t k_page, k_tok, k_head, v_page, v_tok, v_head;  // bytes
     void* kc;
     void* vc;
-    float k_inv, v_inv;  // 1 / scale
+    E4m3Scale k_scale, v_scale;
     // backward: gridDim.x rows of 2 x D partial weight gradients, then their sums
     float* partial;
     float* dwq;
