@@ -358,7 +358,8 @@ tcm_status tcm_lora_workspace(int64_t M, int64_t K, int64_t R, int64_t* bytes);
  * contiguous: element (t, h, d) at ptr[t * token_stride + h * head_stride + d].
  * 16-byte aligned, strides multiples of 8 elements (TCM_ERR_MISALIGNED); so a
  * slice of the heads of a fused projection is a view.  Views that a call writes
- * must not overlap themselves or each other. */
+ * must not overlap themselves or each other.  Here and in a cache, the stride of a
+ * dimension of one element is not looked at, nor are ldx and ldo of one row. */
 typedef struct tcm_heads {
     void* ptr;
     int64_t token_stride, head_stride;

@@ -37,8 +37,10 @@ tcm_status launched(hipError_t e) { return e == hipSuccess ? TCM_OK : TCM_ERR_HI
 // ---- views ----------------------------------------------------------------------
 
 // A stride is not negative, and n steps of it (n >= 0) stay far within 64 bits of bytes.
+// Where n <= 1 no step is taken, and any stride will do.
 bool stride_ok(int64_t n, int64_t stride) {
     int64_t t;
+    if (n <= 1) return true;
     return stride >= 0 && stride <= kMaxStride && !__builtin_mul_overflow(n, stride, &t) &&
            t < (int64_t(1) << 60);
 }
@@ -46,7 +48,7 @@ bool stride_ok(int64_t n, int64_t stride) {
 tcm_status check_heads(const tcm_heads* v, int64_t T, int64_t H) {
     if (!v || !v->ptr) return TCM_ERR_NULL_POINTER;
     if (!stride_ok(T, v->token_stride) || !stride_ok(H, v->head_stride)) return TCM_ERR_INVALID_SHAPE;
-    if (!aligned16(v->ptr) || v->token_stride % 8 != 0 || v->head_stride % 8 != 0)
+    if (!aligned16(v->ptr) || (T > 1 && v->token_stride % 8 != 0) || (H > 1 && v->head_stride % 8 != 0))
         return TCM_ERR_MISALIGNED;
     return TCM_OK;
 }
@@ -67,7 +69,9 @@ tcm_status check_written(const tcm_heads* v, int64_t T, int64_t H, int64_t D) {
     return TCM_OK;
 }
 
-HeadView view(const tcm_heads* v) { return {v->ptr, v->token_stride, v->head_stride}; }
+HeadView view(const tcm_heads* v, int64_t T, int64_t H) {
+    return {v->ptr, T > 1 ? v->token_stride : 0, H > 1 ? v->head_stride : 0};
+}
 
 tcm_status check_cache(const tcm_cache* c, tcm_dtype dtype, int64_t Hk, int64_t D, bool written) {
     if (!c) return TCM_ERR_NULL_POINTER;
@@ -75,9 +79,9 @@ tcm_status check_cache(const tcm_cache* c, tcm_dtype dtype, int64_t Hk, int64_t 
     if (c->pages < 0 || c->page_size < 1) return TCM_ERR_INVALID_SHAPE;
     const int64_t st[6] = {c->k_page_stride, c->k_token_stride, c->k_head_stride,
                            c->v_page_stride, c->v_token_stride, c->v_head_stride};
+    const int64_t count[3] = {c->pages, c->page_size, Hk};
     for (int i = 0; i < 6; ++i)
-        if (!stride_ok(i % 3 == 0 ? c->pages : i % 3 == 1 ? c->page_size : Hk, st[i]))
-            return TCM_ERR_INVALID_SHAPE;
+        if (!stride_ok(count[i % 3], st[i])) return TCM_ERR_INVALID_SHAPE;
     if (written) {
         // every (page, place, head) its own D elements at least
         for (int i = 0; i < 6; i += 3) {
@@ -87,15 +91,18 @@ tcm_status check_cache(const tcm_cache* c, tcm_dtype dtype, int64_t Hk, int64_t 
         }
     }
     if (c->pages > 0 && (!c->k || !c->v)) return TCM_ERR_NULL_POINTER;
-    if (c->pages > INT32_MAX || c->page_size > (int64_t(1) << 20) || c->k_token_stride > kMaxTokenStride ||
-        c->v_token_stride > kMaxTokenStride)
+    if (c->pages > INT32_MAX || c->page_size > (int64_t(1) << 20) ||
+        (c->page_size > 1 && (c->k_token_stride > kMaxTokenStride || c->v_token_stride > kMaxTokenStride)))
         return TCM_ERR_UNSUPPORTED_SHAPE;
     const int64_t piece = c->dtype == TCM_E4M3 ? 16 : 8;
-    for (int64_t s : st)
-        if (s % piece != 0) return TCM_ERR_MISALIGNED;
+    for (int i = 0; i < 6; ++i)
+        if (count[i % 3] > 1 && st[i] % piece != 0) return TCM_ERR_MISALIGNED;
     if (!aligned16(c->k) || !aligned16(c->v)) return TCM_ERR_MISALIGNED;
     return TCM_OK;
 }
+
+// A stride in bytes; none where there is no step of it.
+int64_t step_bytes(int64_t n, int64_t stride, int64_t es) { return n > 1 ? stride * es : 0; }
 
 // log2 of a power of two, -1 of any other page size
 int32_t shift_of(int64_t page_size) {
@@ -277,10 +284,15 @@ tcm_status tcm_lora_gemm_tn(const void* X, int64_t ldx, const void* W, const voi
                             void* workspace, int64_t workspace_bytes, void* stream) {
     if (!half_type(dtype) || !(out_dtype == dtype || out_dtype == TCM_F32))
         return TCM_ERR_UNSUPPORTED_DTYPE;
-    if (N < 0 || L < 0 || ldx < (K > 1 ? K : 1) || ldo < (N > 1 ? N : 1)) return TCM_ERR_INVALID_SHAPE;
+    if (N < 0 || L < 0 || (M != 1 && (ldx < (K > 1 ? K : 1) || ldo < (N > 1 ? N : 1)))) return TCM_ERR_INVALID_SHAPE;
     tcm_status s = check_lora_sizes(M, K, R);
     if (s != TCM_OK) return s;
-    if (N > kMaxRows || L > kMaxRows || ldx > kMaxLd || ldo > INT32_MAX) return TCM_ERR_UNSUPPORTED_SHAPE;
+    if (N > kMaxRows || L > kMaxRows) return TCM_ERR_UNSUPPORTED_SHAPE;
+    if (M == 1) {  // no step from row to row
+        ldx = K;
+        ldo = cdiv(N, 4) * 4;
+    }
+    if (ldx > kMaxLd || ldo > INT32_MAX) return TCM_ERR_UNSUPPORTED_SHAPE;
     if (cdiv(M, 64) * cdiv(N, 64) > INT32_MAX) return TCM_ERR_UNSUPPORTED_SHAPE;
     if (M == 0 || N == 0) return TCM_OK;
     const bool adapters = L > 0 && R > 0 && K > 0;
@@ -329,8 +341,8 @@ tcm_status tcm_qk_norm_rope(const tcm_heads* q, const tcm_heads* k, const tcm_he
     if ((s = device_info(&dev)) != TCM_OK) return s;
     RopeArgs a;
     fill_rope(&a, rope, T, Hq, Hk);
-    if (Hq > 0) a.q = view(q), a.qo = view(q_out);
-    if (Hk > 0) a.k = view(k), a.ko = view(k_out);
+    if (Hq > 0) a.q = view(q, T, Hq), a.qo = view(q_out, T, Hq);
+    if (Hk > 0) a.k = view(k, T, Hk), a.ko = view(k_out, T, Hk);
     return launched(launch_norm_rope(a, (int32_t)dtype, (int32_t)rope->layout, (hipStream_t)stream));
 }
 
@@ -350,8 +362,8 @@ tcm_status tcm_qk_norm_rope_cache(const tcm_heads* q, const tcm_heads* k, const 
     if ((s = device_info(&dev)) != TCM_OK) return s;
     RopeArgs a;
     fill_rope(&a, rope, T, Hq, Hk);
-    if (Hq > 0) a.q = view(q), a.qo = view(q_out);
-    if (Hk > 0) a.k = view(k), a.v = view(v);
+    if (Hq > 0) a.q = view(q, T, Hq), a.qo = view(q_out, T, Hq);
+    if (Hk > 0) a.k = view(k, T, Hk), a.v = view(v, T, Hk);
     a.Hv = (int32_t)Hk;
     a.slots = slots;
     a.num_slots = cache->pages * cache->page_size;
@@ -361,12 +373,12 @@ tcm_status tcm_qk_norm_rope_cache(const tcm_heads* q, const tcm_heads* k, const 
     const int64_t es = a.cache_e4m3 ? 1 : 2;
     a.kc = cache->k;
     a.vc = cache->v;
-    a.k_page = cache->k_page_stride * es;
-    a.k_tok = cache->k_token_stride * es;
-    a.k_head = cache->k_head_stride * es;
-    a.v_page = cache->v_page_stride * es;
-    a.v_tok = cache->v_token_stride * es;
-    a.v_head = cache->v_head_stride * es;
+    a.k_page = step_bytes(cache->pages, cache->k_page_stride, es);
+    a.k_tok = step_bytes(cache->page_size, cache->k_token_stride, es);
+    a.k_head = step_bytes(Hk, cache->k_head_stride, es);
+    a.v_page = step_bytes(cache->pages, cache->v_page_stride, es);
+    a.v_tok = step_bytes(cache->page_size, cache->v_token_stride, es);
+    a.v_head = step_bytes(Hk, cache->v_head_stride, es);
     a.k_scale = scale_parts(cache->k_scale);
     a.v_scale = scale_parts(cache->v_scale);
     return launched(launch_norm_rope(a, (int32_t)dtype, (int32_t)rope->layout, (hipStream_t)stream));
@@ -409,12 +421,12 @@ tcm_status tcm_qk_norm_rope_bwd(const tcm_heads* dq_out, const tcm_heads* dk_out
     RopeArgs a;
     fill_rope(&a, rope, any ? T : 0, Hq, Hk);
     if (any && Hq > 0) {
-        a.dqo = view(dq_out), a.qo = view(dq);
-        if (rope->norm) a.q = view(q);
+        a.dqo = view(dq_out, T, Hq), a.qo = view(dq, T, Hq);
+        if (rope->norm) a.q = view(q, T, Hq);
     }
     if (any && Hk > 0) {
-        a.dko = view(dk_out), a.ko = view(dk);
-        if (rope->norm) a.k = view(k);
+        a.dko = view(dk_out, T, Hk), a.ko = view(dk, T, Hk);
+        if (rope->norm) a.k = view(k, T, Hk);
     }
     a.partial = dw ? (float*)workspace : nullptr;
     a.dwq = dq_weight;
@@ -464,16 +476,16 @@ tcm_status tcm_paged_attention(const tcm_heads* q, const tcm_cache* cache,
     memset(&a, 0, sizeof(a));
     const bool e4m3 = cache->dtype == TCM_E4M3;
     const int64_t es = e4m3 ? 1 : 2;
-    a.q = view(q);
-    a.out = view(out);
+    a.q = view(q, B, Hq);
+    a.out = view(out, B, Hq);
     a.kc = (const char*)cache->k;
     a.vc = (const char*)cache->v;
-    a.k_page = cache->k_page_stride * es;
-    a.k_tok = cache->k_token_stride * es;
-    a.k_head = cache->k_head_stride * es;
-    a.v_page = cache->v_page_stride * es;
-    a.v_tok = cache->v_token_stride * es;
-    a.v_head = cache->v_head_stride * es;
+    a.k_page = step_bytes(cache->pages, cache->k_page_stride, es);
+    a.k_tok = step_bytes(cache->page_size, cache->k_token_stride, es);
+    a.k_head = step_bytes(Hk, cache->k_head_stride, es);
+    a.v_page = step_bytes(cache->pages, cache->v_page_stride, es);
+    a.v_tok = step_bytes(cache->page_size, cache->v_token_stride, es);
+    a.v_head = step_bytes(Hk, cache->v_head_stride, es);
     a.table = block_table;
     a.table_stride = table_stride;
     a.lengths = lengths;

@@ -168,10 +168,7 @@ def lora_gemm_tn(x, w, lora_a, lora_b, row_adapter, scales=None, ranks=None, out
     xs, os = x.stride(), out.stride()
     if (K > 1 and xs[1] != 1) or (N > 1 and os[1] != 1):
         raise ValueError("x and out need contiguous rows")
-    ldx = xs[0] if M > 1 else max(xs[0], K, 1)
-    ldo = os[0] if M > 1 else max(os[0], N, 1)
-    if M <= 1 and ldx % 8:
-        ldx = max(K, 1)
+    ldx, ldo = (xs[0], os[0]) if M else (max(K, 1), max(N, 1))
     ws, nbytes, keep = _workspace(workspace, dev, lora_workspace, M, K, R)
     _run(dev, lib().tcm_lora_gemm_tn, x.data_ptr(), ldx, wp, ap, bp, rp, kp, sp, out.data_ptr(), ldo,
          M, N, K, L, R, code, _OUT[out.dtype], ws, nbytes)
