@@ -464,7 +464,8 @@ tcm_status tcm_paged_attention(const tcm_heads* q, const tcm_cache* cache,
     // the first tile of a window begins up to 31 keys before it
     const int64_t span = window > 0 && window + 31 < max_len ? window + 31 : max_len;
     const Split sp = split_of(B, Hq, Hk, span);
-    if (B * Hk * cdiv(Hq / Hk, 16) > INT32_MAX / sp.n) return TCM_ERR_UNSUPPORTED_SHAPE;  // workgroups
+    // a launch holds less than 2^32 threads
+    if (B * Hk * cdiv(Hq / Hk, 16) > (int64_t)(UINT32_MAX / 256) / sp.n) return TCM_ERR_UNSUPPORTED_SHAPE;
     if (sp.n > 1) {
         if (!workspace) return TCM_ERR_NULL_POINTER;
         if (!aligned16(workspace)) return TCM_ERR_MISALIGNED;
