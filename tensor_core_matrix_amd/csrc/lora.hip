@@ -494,12 +494,18 @@ void product(const LoraArgs& a, int cus, hipStream_t st) {
     }
     if (mb <= 4) return;
     // The largest tile that still gives every compute unit one (128 x 64: three in
-    // four of them), as what a unit reads into LDS is what bounds the small ones.
-    // us without adapters, rows of 4096 x 4096: 4096 rows 256 x 256 114, 128 x 128 134,
-    // 128 x 64 165; 2048 rows 112, 71 and 87; 333 rows 128 x 64 25, 64 x 64 31; 128
-    // rows 24 and 17.
+    // four of them), as what a unit reads into LDS is what bounds the small ones; and
+    // of 256 x 256, which are one a unit at a time, not so few in the last round that
+    // more than a quarter of the rounds idles.  us with an adapter a request, rank 16,
+    // K = 4096:
+    //   256 x 256 and 128 x 128: 4096 x 4096 (256 tiles) 129 and 156; 4352 x 4096 (272) 224
+    //     and 176; 6144 x 4096 (384) 229 and 222; 6400 x 4096 (400) 231 and 245; 8192 x 4096
+    //     (512) 249 and 298; 8448 x 4096 (528) 344 and 315; 9984 x 4096 (624) 345 and 357
+    //   128 x 128 and 128 x 64: 2048 x 2048 (256 tiles) 55 and 58; 4096 x 2048 81 and 110
+    //   128 x 64 and 64 x 64: 333 x 4096 (192 tiles) 33 and 40; 256 x 4096 (128) 33 and 25
     auto count = [&](int64_t bm, int64_t bn) { return (int64_t)cdiv_i(a.M, bm) * cdiv_i(a.N, bn); };
-    if (count(256, 256) >= cus)
+    const int64_t large = count(256, 256), rounds = cdiv_i(large, cus);
+    if (large >= cus && 4 * large > 3 * rounds * cus)
         tiles<T, TO, 256, 256, 2, 4, 2, 1>(a, st);
     else if (count(128, 128) >= cus)
         tiles<T, TO, 128, 128, 2, 2, 2, 1>(a, st);
