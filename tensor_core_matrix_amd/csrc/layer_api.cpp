@@ -166,16 +166,21 @@ int64_t bwd_workspace(int64_t D) { return int64_t(kRopeBwdGrid) * 2 * D * 4; }
 // The split over the length.  Two ways to deal the work to workgroups of four waves:
 //  * heads == 1: a chunk of one key-value head's keys, its tiles dealt to the
 //    waves.  Chunks of 1024 keys, or fewer (256 at least) where that leaves fewer than
-//    1024 workgroups: 64 sequences of up to 4096 keys take 100 us in chunks of 1024,
+//    1024 workgroups: 64 sequences of up to 4096 keys took 100 us in chunks of 1024,
 //    101 of 768 and 107 of 2048 (lengths differ: the last chunks idle the device);
 //    32 of up to 8192 E4M3 keys 67, and 72 in chunks of 512 (each pays its first
 //    reads' latency).
 //  * heads == 4: the same chunk of four heads, one a wave, so that the
 //    workgroup reads whole stretches of memory (a probe that only reads reaches
-//    6.9 TB/s that way and 6.4 with a head a workgroup).  One sequence of 131001
-//    keys takes 87 us, and 93 the other way; 64 of different lengths 106.  So it
-//    is for few sequences with work for every compute unit.
-constexpr int64_t kMinChunk = 256, kChunk = 1024;
+//    6.9 TB/s that way and 6.4 with a head a workgroup).  It is for few sequences with
+//    work for every one of 256 compute units.  us this way and the other, 8 key-value
+//    heads of 128: 1 sequence of 131072 keys (256 workgroups) 87 and 94, of 65536 (128)
+//    62 and 52; 4 of 32768 (256) 87 and 93, of which three are shorter 64 and 64, of
+//    16384 (128) 62 and 51; beyond four sequences both sides come near: 8 of 16384
+//    (256) 87 and 93, 16 of up to 16384 (512) 118 and 109, 32 of up to 8192 123 and 118.
+// A launch holds less than 2^32 threads, 256 a workgroup: where the chunks of very many
+// sequences and heads would pass that, they are longer.
+constexpr int64_t kMinChunk = 256, kChunk = 1024, kMostGroups = UINT32_MAX / 256;
 struct Split {
     int64_t chunk, n, heads;
 };
@@ -191,7 +196,10 @@ Split split_of(int64_t B, int64_t Hq, int64_t Hk, int64_t span) {
         const int64_t c = cdiv(cdiv(span, cdiv(1024, split_units(B, Hq, Hk))), 128) * 128;
         s.chunk = c < kMinChunk ? kMinChunk : c < kChunk ? c : kChunk;
     }
-    if (cdiv(span, s.chunk) > kAttnMaxSplits) s.chunk = cdiv(cdiv(span, kAttnMaxSplits), 128) * 128;
+    int64_t most = kMostGroups / split_units(B, Hq, Hk);
+    if (most > kAttnMaxSplits) most = kAttnMaxSplits;
+    if (most < 1) most = 1;
+    if (cdiv(span, s.chunk) > most) s.chunk = cdiv(cdiv(span, most), 128) * 128;
     s.n = cdiv(span, s.chunk);
     if (s.n < 1) s.n = 1;
     return s;
@@ -464,8 +472,7 @@ tcm_status tcm_paged_attention(const tcm_heads* q, const tcm_cache* cache,
     // the first tile of a window begins up to 31 keys before it
     const int64_t span = window > 0 && window + 31 < max_len ? window + 31 : max_len;
     const Split sp = split_of(B, Hq, Hk, span);
-    // a launch holds less than 2^32 threads
-    if (B * Hk * cdiv(Hq / Hk, 16) > (int64_t)(UINT32_MAX / 256) / sp.n) return TCM_ERR_UNSUPPORTED_SHAPE;
+    if (split_units(B, Hq, Hk) > kMostGroups / sp.n) return TCM_ERR_UNSUPPORTED_SHAPE;
     if (sp.n > 1) {
         if (!workspace) return TCM_ERR_NULL_POINTER;
         if (!aligned16(workspace)) return TCM_ERR_MISALIGNED;
