@@ -16,15 +16,15 @@
 // input without leaving its lane.  V is read 8 keys x D / 16 elements a lane
 // (lane c = l % 16 takes elements c D / 16 .. of each of its 8 keys, so 16 lanes
 // read a whole row), and turned into the 8-keys-of-one-element form by byte
-// permutations within the lane.  A probability is rounded to the type's 8 or 11 bits
+// permutations within the lane.  A probability is cut to the type's 8 or 11 bits
 // there, and what that leaves is rounded and multiplied too: 16 or 22 bits together, so
 // that the result's error is its own rounding (one product in bf16: a third more).  The
-// second products cost 1 to 2 % (64 sequences of up to 4096 keys 102.5 us, and 100.8
-// without).
-// Maximum and sum of a head's softmax live in its lanes too.  K is read in whole rows and goes through the wave's own LDS
-// area: read in the operand's pattern of 16 rows x 64 bytes, memory gives 5.2 TB/s
-// to a kernel that does nothing else, in whole rows 6.4.  Nothing waits for another
-// wave until a workgroup's four join at the end.
+// second products cost up to 1.5 % (64 sequences of up to 4096 keys 101.6 us, and 101.1
+// without; 32 of up to 8192 in E4M3 68.0 and 67.0), 1 to 3 with heads above 128.
+// Maximum and sum of a head's softmax live in its lanes too.  K is read in whole rows
+// and goes through the wave's own LDS area: read in the operand's pattern of 16 rows x
+// 64 bytes, memory gives 5.2 TB/s to a kernel that does nothing else, in whole rows
+// 6.4.  Nothing waits for another wave until a workgroup's four join at the end.
 //
 // A workgroup takes a chunk of a sequence's keys, for one key-value head with its
 // tiles dealt to the four waves or for four heads, one a wave; the next tile's
@@ -32,8 +32,8 @@
 // chunk the partial results go to the workspace and attn_join_kernel joins them.
 //
 // Bound by reads: one sequence of 131001 keys (32 query, 8 key-value heads of 128,
-// fp16) takes 85 us, 6.3 TB/s, and 5 for the join; 64 sequences of up to 4096 keys
-// 97 us, 5.8 TB/s; 32 of up to 8192 in E4M3 62 us, 4.9 TB/s; 200 keys 7.5 us.
+// fp16) takes 86 us, 6.3 TB/s, and 5 for the join; 64 sequences of up to 4096 keys
+// 98 us, 5.6 TB/s; 32 of up to 8192 in E4M3 63 us, 4.8 TB/s; 200 keys 8.1 us.
 #include <type_traits>
 
 #include "layer_internal.h"
@@ -50,10 +50,21 @@ constexpr float kNegInf = -__builtin_inff();
 // result is divided by it where the waves' parts meet.  They are at most 1, and fp16 ends at
 // 2^-24: as they are, thousands of keys 2^-25 below the largest would vanish from the
 // product and count in the sum.  bf16 has fp32's exponents.
+// parts: two probabilities, times kLift, as upper parts (cut off) and lower parts (rounded).
+// The upper one is cut from a number a little smaller, so that the lower one is
+// never zero, and both are positive: an infinite value times them is infinite.  (fp16
+// ends before it for probabilities below 2^-26.)
 template <class T> struct Half16;
 template <> struct Half16<__bf16> {
-    static constexpr float kLift = 1.0f;
+    static constexpr float kLift = 1.0f, kBelow = 0x1.fffff8p-1f;  // 1 - 2^-22
     typedef bf16x8_t x8;
+    __device__ static __forceinline__ void parts(float e0, float e1, uint32_t& upper, uint32_t& lower) {
+        const uint32_t b0 = __float_as_uint(e0 * kBelow), b1 = __float_as_uint(e1 * kBelow);
+        upper = __builtin_amdgcn_perm(b1, b0, 0x07060302);
+        typedef __bf16 pair __attribute__((ext_vector_type(2)));
+        const pair r = {(__bf16)(e0 - __uint_as_float(b0 & 0xffff0000u)), (__bf16)(e1 - __uint_as_float(b1 & 0xffff0000u))};
+        lower = __builtin_bit_cast(uint32_t, r);
+    }
     __device__ static __forceinline__ f32x4_t mma(x8 a, x8 b, f32x4_t c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
     }
@@ -63,8 +74,14 @@ template <> struct Half16<__bf16> {
     }
 };
 template <> struct Half16<_Float16> {
-    static constexpr float kLift = 32768.0f;
+    static constexpr float kLift = 32768.0f, kBelow = 32768.0f - 2.0f;  // (1 - 2^-14)
     typedef f16x8_t x8;
+    __device__ static __forceinline__ void parts(float e0, float e1, uint32_t& upper, uint32_t& lower) {
+        const auto u = __builtin_amdgcn_cvt_pkrtz(e0 * kBelow, e1 * kBelow);
+        upper = __builtin_bit_cast(uint32_t, u);
+        const f16x2_t r = {(_Float16)fmaf(e0, kLift, -(float)u[0]), (_Float16)fmaf(e1, kLift, -(float)u[1])};
+        lower = __builtin_bit_cast(uint32_t, r);
+    }
     __device__ static __forceinline__ f32x4_t mma(x8 a, x8 b, f32x4_t c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
     }
@@ -297,9 +314,8 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : DP == 128 && E4M3 && ALIGNED ?
     for (int m = 0; m < VE; ++m) o[m] = (f32x4_t){};
     float mx = kNegInf, sum = 0.0f;
 
-    // (`next` asks for the next tile's keys, once the registers of these are free;
-    // `upper`: what a probability's upper part is rounded from)
-    auto compute = [&](Keys& kt, Values& t, const Where& w, int key0, float upper, auto&& next) {
+    // (`next` asks for the next tile's keys, once the registers of these are free)
+    auto compute = [&](Keys& kt, Values& t, const Where& w, int key0, auto&& next) {
         // a tile with unusable keys: their scores become -infinity and, since a
         // probability of 0 times what lies in such a place may be NaN, their
         // values 0
@@ -382,14 +398,15 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : DP == 128 && E4M3 && ALIGNED ?
                 for (int i = 0; i < 4; ++i) o[m][i] *= f;
         }
         const float m0 = mx == kNegInf ? 0.0f : mx;
-        x8 pf, pr;
+        uint32_t pu[4], pl[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float e = __builtin_amdgcn_exp2f(x[j] - m0);
-            sum += e;
-            pf[j] = (T)(e * upper);
-            pr[j] = (T)(e * H::kLift - (float)pf[j]);
+        for (int j = 0; j < 8; j += 2) {
+            const float e0 = __builtin_amdgcn_exp2f(x[j] - m0), e1 = __builtin_amdgcn_exp2f(x[j + 1] - m0);
+            sum += e0;
+            sum += e1;
+            H::parts(e0, e1, pu[j / 2], pl[j / 2]);
         }
+        const x8 upper = __builtin_bit_cast(x8, *(i32x4_t*)pu), lower = __builtin_bit_cast(x8, *(i32x4_t*)pl);
         // 8 keys x VE elements -> VE operands of 8 keys
 #pragma unroll
         for (int m = 0; m < VE; m += 2) {
@@ -408,10 +425,10 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : DP == 128 && E4M3 && ALIGNED ?
                 hi[jj] = __builtin_amdgcn_perm(v1, v0, 0x07060302);
             }
             const x8 v0 = __builtin_bit_cast(x8, *(i32x4_t*)lo), v1 = __builtin_bit_cast(x8, *(i32x4_t*)hi);
-            o[m] = H::mma(v0, pf, o[m]);
-            o[m + 1] = H::mma(v1, pf, o[m + 1]);
-            o[m] = H::mma(v0, pr, o[m]);
-            o[m + 1] = H::mma(v1, pr, o[m + 1]);
+            o[m] = H::mma(v0, upper, o[m]);
+            o[m + 1] = H::mma(v1, upper, o[m + 1]);
+            o[m] = H::mma(v0, lower, o[m]);
+            o[m + 1] = H::mma(v1, lower, o[m + 1]);
         }
     };
 
@@ -420,55 +437,36 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : DP == 128 && E4M3 && ALIGNED ?
     // keys are free as soon as they are in LDS), and its successor's pages are
     // looked up (asked for before those loads, so that waiting for them is no wait
     // for the loads).
-    // An infinite value times a lower part that is zero, or has the other sign, is NaN where
-    // the sum is infinite: a wave that ends with one (E4M3 has no infinities) goes over its
-    // keys again, for the heads that have one with parts that are both half of a
-    // probability, and one sign; the others come to the same bits.
-    for (float upper = H::kLift;;) {
-        int key = start + 32 * kw;
-        if (key < end) {
-            Keys kt;
-            Values va, vb;
-            Where wa = look(key), wb = look(key + round), wc;
-            settle(wa);
-            load_keys(kt, wa);
-            load_values(va, wa);
-            for (;;) {
-                settle(wb);
-                wc = look(key + 2 * round);
-                bool more = key + round < end;
-                if (more) load_values(vb, wb);
-                compute(kt, va, wa, key, upper, [&] {
-                    if (more) load_keys(kt, wb);
-                });
-                if (!more) break;
-                key += round;
-                settle(wc);
-                wa = look(key + 2 * round);
-                more = key + round < end;
-                if (more) load_values(va, wc);
-                compute(kt, vb, wb, key, upper, [&] {
-                    if (more) load_keys(kt, wc);
-                });
-                if (!more) break;
-                key += round;
-                wb = wa;
-                wa = wc;
-            }
+    int key = start + 32 * kw;
+    if (key < end) {
+        Keys kt;
+        Values va, vb;
+        Where wa = look(key), wb = look(key + round), wc;
+        settle(wa);
+        load_keys(kt, wa);
+        load_values(va, wa);
+        for (;;) {
+            settle(wb);
+            wc = look(key + 2 * round);
+            bool more = key + round < end;
+            if (more) load_values(vb, wb);
+            compute(kt, va, wa, key, [&] {
+                if (more) load_keys(kt, wb);
+            });
+            if (!more) break;
+            key += round;
+            settle(wc);
+            wa = look(key + 2 * round);
+            more = key + round < end;
+            if (more) load_values(va, wc);
+            compute(kt, vb, wb, key, [&] {
+                if (more) load_keys(kt, wc);
+            });
+            if (!more) break;
+            key += round;
+            wb = wa;
+            wa = wc;
         }
-        if (E4M3 || __any(upper != H::kLift)) break;
-        bool nan = false;
-#pragma unroll
-        for (int m = 0; m < VE; ++m)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) nan |= o[m][i] != o[m][i];
-        const uint64_t in = __ballot(nan);
-        if (!in) break;
-        if (in >> r16 & 0x0001000100010001u) upper = 0.5f * H::kLift;
-#pragma unroll
-        for (int m = 0; m < VE; ++m) o[m] = (f32x4_t){};
-        mx = kNegInf;
-        sum = 0.0f;
     }
 
     // ---- the four waves' parts ------------------------------------------------

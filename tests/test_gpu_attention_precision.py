@@ -3,9 +3,9 @@ for probabilities of 8 or 11 bits.
 
 A score is an fp32 sum of D products, off by at most (2 D + 8) 2^-24 of the largest sum of
 magnitudes of its row, and so is the exponent of its probability, whose exponential adds 2^-20; a
-probability enters its product as two values of the type, off by 2^-17 (bf16: twice 8 bits and a
-rounding each) or 2^-22 (fp16) of itself, and by 2^-40 of the row's largest (fp16's smallest
-number, times 2^-15); its sums are fp32, over at most a tile's 32 keys of a chunk's turns and the
+probability enters its product as two values of the type, off by at most 2^-16 (bf16) or 2^-21
+(fp16) of itself, half of which is asked of a sum of them, and by 2^-40 of the row's largest
+(fp16's smallest number, times 2^-15); its sums are fp32, over at most a tile's 32 keys of a chunk's turns and the
 joins; then the output is rounded once.
 """
 import math
@@ -88,7 +88,7 @@ def test_infinite_values(n, page, dt):
     assert torch.isnan(out[0, :2, 33]).all()
     assert (torch.isneginf(out[0, :2, 50]) if first == last else torch.isnan(out[0, :2, 50])).all()
     rest = [d for d in range(D) if d not in (3, 20, 33, 50)]
-    step = 2.0 ** (-8 if dt is torch.bfloat16 else -11)  # (the keys may have gone without their lower halves)
+    step = 2.0 ** (-8 if dt is torch.bfloat16 else -11)  # (room for a form that rounds probabilities once)
     size = want.float().abs().max()
     assert ((out[0, :2, rest].float() - want[0, :2, rest].float()).abs() <= 2 * step * size).all()
     assert torch.equal(out[0, 2:], want[0, 2:]) and torch.equal(out[1], want[1])
