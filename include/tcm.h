@@ -339,9 +339,8 @@ tcm_status tcm_plan_gemm(int64_t batch, int64_t M, int64_t N, int64_t K, tcm_dty
  * inner product X[i] . A_a^T (times s_a) enters the second product as a sum of
  * two 16-bit values, which hold 16 bits of it (TCM_F16: 22 bits of the largest
  * of 16 consecutive ranks; fp32 outputs of TCM_BF16: three values, 24 bits),
- * whatever its size.  A row's output
- * depends on its own adapter only: values that are not finite in one adapter
- * do not reach the rows of another.
+ * whatever its size.  A row's output depends on its own adapter only: values
+ * that are not finite in one adapter do not reach the rows of another.
  * R a multiple of 8, at most 128; K a multiple of 8 (TCM_ERR_MISALIGNED
  * otherwise); ldx a multiple of 8 and at most 2^21; X, W, A, B and Out 16-byte
  * aligned; Out overlaps no input.  L == 0 or R == 0 gives the projection alone.

@@ -7,8 +7,9 @@
 // a 32-deep product holds 16 ranks twice, the upper halves of t in inner
 // positions 0..15 and what they leave in 16..31, against the same 16 columns
 // of B_a.  (One rounded t would add an error of the size of the output's own
-// rounding where the adapter is as large as the projection; the second half
-// costs nothing below rank 32 and little above it.)  For fp32 outputs of bf16
+// rounding where the adapter is as large as the projection.  The second half costs
+// nothing up to rank 16, whose product is 32 deep anyway, and from there twice the
+// products, which are few beside the projection's.)  For fp32 outputs of bf16
 // operands a second product adds what the two halves leave.
 //
 // A row's 16 values are multiplied by a power of two first, which brings the largest of
@@ -25,15 +26,24 @@
 
 namespace tcm {
 
+// cut: x in the type, cut off a little nearer zero, so that what it leaves is never zero and
+// has x's sign: an infinite element of B_a then gives its rows infinities, not NaN.
 template <class T> struct LoraMma;
 template <> struct LoraMma<__bf16> {
     typedef bf16x8_t x8;
+    __device__ static __forceinline__ __bf16 cut(float x) {
+        const uint32_t b = __float_as_uint(x * 0x1.fffff8p-1f);  // 1 - 2^-22
+        return __builtin_bit_cast(__bf16, (uint16_t)(b >> 16));
+    }
     __device__ static __forceinline__ f32x4_t mma(x8 a, x8 b, f32x4_t c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
     }
 };
 template <> struct LoraMma<_Float16> {
     typedef f16x8_t x8;
+    __device__ static __forceinline__ _Float16 cut(float x) {
+        return (_Float16)__builtin_amdgcn_cvt_pkrtz(x * 0x1.fff8p-1f, 0.0f)[0];  // 1 - 2^-14
+    }
     __device__ static __forceinline__ f32x4_t mma(x8 a, x8 b, f32x4_t c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
     }
@@ -77,7 +87,7 @@ __device__ __forceinline__ f32x8 lora_t8(const LoraArgs& p, int m, int r) {
 // The t operand of ranks r0 .. r0 + 15 of the block's rows: lane l holds row
 // l % 16, ranks r0 + 8 (g % 2) + 0..7 of the upper (g < 2) or lower half, g = l / 16.
 // Lanes whose row is not `mine` get zeros (their t was never written).  rest: what
-// the two halves leave, and zeros beside it (FULL).  up: what the row's products are
+// the two halves leave, half of it in each (FULL).  up: what the row's products are
 // multiplied by.
 template <class T> struct LoraT {
     typename LoraMma<T>::x8 f, rest;
@@ -101,14 +111,14 @@ __device__ __forceinline__ LoraT<T> lora_t(const LoraArgs& p, int m, int r0, int
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const float x = t[j] * down;
-        const T hi = convert_out<T>(x);
+        const T hi = LoraMma<T>::cut(x);
         const float rest = x - (float)hi;
         // (an infinite or NaN upper half, which is t itself, says all)
-        const T lo = rest == rest ? convert_out<T>(rest) : (T)0.0f;
+        const T lo = rest != rest ? (T)0.0f : FULL ? LoraMma<T>::cut(rest) : convert_out<T>(rest);
         o.f[j] = g4 < 2 ? hi : lo;
         if constexpr (FULL) {
             const float last = rest - (float)lo;
-            o.rest[j] = g4 < 2 && last == last ? convert_out<T>(last) : (T)0.0f;
+            o.rest[j] = last == last ? convert_out<T>(0.5f * last) : (T)0.0f;
         }
     }
     return o;
@@ -138,7 +148,8 @@ __device__ __forceinline__ typename LoraMma<T>::x8 lora_b(const LoraArgs& p, int
 // (a decode batch: nearly every row its own) is left to its lanes, each of which
 // adds up its own columns of its own row's adapter in fp32, all of a block's reads
 // under way together: adapter by adapter, 128 rows with 64 adapters (4096 x 4096,
-// rank 16) take 71 us, this way 33.
+// rank 16) take 71 us, this way 29 (16 without adapters; 78 at rank 64, whose every 8
+// ranks wait for their reads).
 template <class T, bool FULL, int NI, int NJ>
 __device__ __forceinline__ void lora_add(const LoraArgs& p, f32x4_t (&acc)[NI][NJ], int m0, int n0) {
     typedef LoraMma<T> O;
