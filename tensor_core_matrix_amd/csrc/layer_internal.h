@@ -79,7 +79,7 @@ struct AttnArgs {
     int32_t page_shift;  // log2 of page_size where it is a power of two, else -1
     int32_t max_len, window;
     int32_t chunk, splits;
-    int32_t heads;    // key-value heads of a workgroup: 1, 2 or 4, one a wave
+    int32_t heads;    // key-value heads of a workgroup: 1, or 4, one a wave
     int32_t qblocks;  // blocks of 16 query heads of one key-value head
     float scale_log2, v_scale;
 };

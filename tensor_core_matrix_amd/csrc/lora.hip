@@ -5,9 +5,10 @@
 // have an adapter; the product kernel adds t B_a^T to its accumulators before
 // the one rounding (lora_tail.h).  Up to 64 rows the product is bound by reading W
 // (lora_rows_kernel: one row of 4096 x 4096 3.3 + 8.5 us, 3.9 TB/s; 48 rows of 8192 x
-// 4096 with nearly as many adapters of rank 32 6.4 + 31 us), beyond them by what a
-// compute unit reads into LDS and then by the matrix cores (lora_tile_kernel: 333 rows
-// of 4096 x 4096 5.3 + 30 us, 4096 rows 12 + 115 us, 114 us without adapters).
+// 4096 with nearly as many adapters of rank 32 6.2 + 31 us, 23 without adapters), beyond
+// them by what a compute unit reads into LDS and then by the matrix cores
+// (lora_tile_kernel: 333 rows of 4096 x 4096 5.3 + 29 us, 25 without adapters; 4096 rows
+// 12 + 125 us as traced and 128 a call among others, 120 without adapters).
 #include <type_traits>
 
 #include "layer_internal.h"

@@ -10,8 +10,8 @@
 // every access is 16 bytes and a head's two halves are contiguous over its
 // lanes; and as what is done once a head and lane -- the sum, the root, the
 // addresses -- is half of the instructions, few lanes a head count as much
-// (8191 tokens of 32 + 8 + 8 heads of 128, E4M3 cache: 42 us, 4.4 TB/s, and 77 with
-// E = 4; backwards 8192 tokens of 32 + 8 heads 52 us, 4.8 TB/s, and 5 for the sums).
+// (8191 tokens of 32 + 8 + 8 heads of 128, E4M3 cache: 42 us, 4.3 TB/s, and 77 with
+// E = 4; backwards 8192 tokens of 32 + 8 heads 52 us, 4.9 TB/s, and 5 for the sums).
 // The angles of a workgroup's tokens are computed once, by its threads, into
 // LDS: position * inv_freq in two times 64 bits, reduced to one turn there and only then
 // rounded, so a position near 2^31 is as good as one near 0 and no table has to
