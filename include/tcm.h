@@ -88,7 +88,8 @@ typedef enum tcm_dtype {
     TCM_E2M1 = 5, /* OCP FP4 E2M1, two per byte, element 2t in the low four bits of
                      byte t (no infinities, no NaN, max 6) */
     TCM_E2M3 = 6, /* OCP FP6 E2M3 (bias 1, 3 mantissa bits, max 7.5), packed: see below */
-    TCM_E3M2 = 7  /* OCP FP6 E3M2 (bias 3, 2 mantissa bits, max 28), packed: see below */
+    TCM_E3M2 = 7, /* OCP FP6 E3M2 (bias 3, 2 mantissa bits, max 28), packed: see below */
+    TCM_U4 = 8    /* unsigned whole numbers 0 .. 15, two per byte as TCM_E2M1 */
 } tcm_dtype;
 
 /* Arrangement of a matrix in memory: row-major (the elements of one row
@@ -489,6 +490,157 @@ tcm_status tcm_paged_attention(const tcm_heads* q, const tcm_cache* cache,
 /* (enough also for smaller B and max_len and for every window) */
 tcm_status tcm_paged_attention_workspace(int64_t B, int64_t Hq, int64_t Hk, int64_t D,
                                          int64_t max_len, int64_t* bytes);
+
+/* ---------------------------------------------------------------------------
+ * A step that drafts several tokens at once: pages and slots for them, the
+ * residual sum and norm before a product, products of few rows with 4-bit
+ * weights, and the attention of the drafted tokens over the cache.  The
+ * conventions are those of the layer operators above.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * The lengths of B sequences change, and pages and slots with them.  Sequence b
+ * of n = lengths[b] keys (clipped to 0 .. table_width * page_size) gets
+ * n' = n + change[b] (clipped the same way), and of its row of the block table
+ *   - entries ceil(n' / page_size) .. ceil(n / page_size) - 1, if there are any, are
+ *     set to -1, and the pages in them (0 .. pages-1; others are no pages) go back to
+ *     the stack of free pages;
+ *   - entries ceil(n / page_size) .. ceil(n' / page_size) - 1 get pages from it, or
+ *     -1 when it has no more.
+ * First all pages are returned, then all are taken, both in the order of (sequence,
+ * entry): with F pages on the stack (the last one, free_pages[F-1], is its top) and R
+ * returned, the r-th goes to free_pages[F + R - 1 - r] (past `capacity`: it is lost,
+ * so let capacity be `pages`), and with F' then there the i-th taken is free_pages[F' - 1 - i].
+ * So a call with the opposite changes right after puts everything back as it was
+ * (unless pages were missing or a length was clipped).
+ *   lengths, change  B int32; lengths is overwritten with n'
+ *   block_table  B rows of table_width entries, table_stride apart, overwritten
+ *   free_pages  capacity int32, free_count one (clipped to 0 .. capacity), overwritten
+ *   starts   B + 1 int32: starts[b] is the sum of the new tokens max(0, n' - n) of
+ *            the sequences before b (at most 2^31 - 1), so token starts[b] + i is number i of b's
+ *   slots, positions  T int32 (or NULL): of every token its position n + i, and its
+ *            slot page * page_size + place there, -1 where its page is missing; rows
+ *            behind the last token get slot -1 and position 0.  Tokens from T on
+ *            have their pages and are in starts, and nothing else is written of them
+ *   missing  NULL, or one int32: the pages that the stack did not have
+ * All results are exact and the same whatever the order of execution.  The arrays that
+ * are written overlap nothing.  page_size at most 2^20, pages * page_size less than 2^31, B at most
+ * 65535, table_width * page_size and T at most 2^30 (TCM_ERR_UNSUPPORTED_SHAPE).
+ */
+tcm_status tcm_cache_plan(int32_t* lengths, const int32_t* change, int32_t* block_table,
+                          int64_t table_stride, int64_t table_width, int64_t B, int64_t pages,
+                          int64_t page_size, int32_t* free_pages, int64_t capacity,
+                          int32_t* free_count, int32_t* starts, int32_t* slots, int32_t* positions,
+                          int64_t T, int32_t* missing, void* stream);
+
+/*
+ * s = X + residual (X where residual is NULL) and Out = w s / sqrt(mean(s^2) + eps)
+ * for every row; the norm is that of the sum before it is rounded.
+ *   X        T x D of `dtype` (TCM_F16 or TCM_BF16), rows ldx >= D elements apart
+ *   residual NULL, or T x D the same way, rows ldr apart
+ *   weight   NULL (ones), or D elements of weight_dtype: TCM_F32 or dtype
+ *   sum      NULL, or T x D of dtype, rows lds apart: s rounded once
+ *   Out      T x D of out_dtype (dtype or TCM_F32), rows ldo apart
+ * Computed in fp32.  sum may be X or residual, and so may Out of the same type (the same
+ * pointer and row stride); Out and sum overlap nothing else.  D a multiple of 8
+ * (TCM_ERR_MISALIGNED), at most 32768; 16-byte aligned, row strides multiples of
+ * 8 elements (16 bytes); a stride is not looked at where T <= 1.
+ */
+tcm_status tcm_add_rms_norm(const void* X, int64_t ldx, const void* residual, int64_t ldr,
+                            const void* weight, tcm_dtype weight_dtype, float eps, void* sum,
+                            int64_t lds, void* Out, int64_t ldo, int64_t T, int64_t D,
+                            tcm_dtype dtype, tcm_dtype out_dtype, void* stream);
+
+/*
+ * The same with the result as tcm_gemm_mx_fp8 takes it: Out T x D E4M3 bytes and
+ * scale T x (D / 32) E8M0 bytes (both dense).  The scale of 32 elements is the smallest
+ * 2^e, e >= -127, with |element| <= 448 * 2^e for every one that is finite; the fp32
+ * quotient is exact and rounded once to nearest even.  An element that is not finite is
+ * NaN.  D a multiple of 32 (TCM_ERR_MISALIGNED).  Out and scale overlap nothing.
+ */
+tcm_status tcm_add_rms_norm_mx_fp8(const void* X, int64_t ldx, const void* residual, int64_t ldr,
+                                   const void* weight, tcm_dtype weight_dtype, float eps,
+                                   void* sum, int64_t lds, void* Out, void* scale, int64_t T,
+                                   int64_t D, tcm_dtype dtype, void* stream);
+
+/*
+ * Gradients: from dOut (of Out), dsum (of the kept sum; NULL: none) and the sum S, those
+ * of X (and of the residual, which is the same), dX, rounded once to dtype, and of the
+ * weight, dweight (D fp32, a sum over the rows, overwritten; NULL: not computed).  With
+ * g = w dOut and h = S / sqrt(mean(S^2) + eps):
+ *   dX = (g - h mean(g h)) / sqrt(mean(S^2) + eps) + dsum,  dweight = sum dOut h.
+ * Sums run in a fixed order: the same call gives the same bits.  dX may be dOut,
+ * dsum or S.  T == 0 gives a zero dweight.
+ */
+tcm_status tcm_add_rms_norm_bwd(const void* dOut, int64_t lddo, const void* dsum, int64_t ldds,
+                                const void* S, int64_t lds, const void* weight,
+                                tcm_dtype weight_dtype, float eps, void* dX, int64_t lddx,
+                                float* dweight, int64_t T, int64_t D, tcm_dtype dtype,
+                                void* workspace, int64_t workspace_bytes, void* stream);
+/* (what a dweight needs; enough also for fewer rows) */
+tcm_status tcm_add_rms_norm_bwd_workspace(int64_t T, int64_t D, int64_t* bytes);
+
+/*
+ * Out = X . W^T with 4-bit weights, for few rows X (single tokens, drafts).
+ *   X        M x K of `dtype` (TCM_F16 or TCM_BF16), rows ldx >= K elements apart
+ *   W        N x K 4-bit elements stored N x (K/2) bytes, element 2t in the low
+ *            four bits of byte t (dense)
+ *   elem TCM_U4:   W[n][k] = scale[n][k / group] * (q - zero[n][k / group]), q = 0 .. 15;
+ *            scales N x (K / group) of dtype, zeros N x (K / group) bytes or NULL (8);
+ *            group a multiple of 32 that divides K
+ *   elem TCM_E2M1: W[n][k] = 2^(scale[n][k / 32] - 127) * element, scales N x (K / 32)
+ *            E8M0 bytes (255: NaN), as tcm_gemm_mx_fp4 takes them; group 32, zeros NULL
+ *   Out      M x N of out_dtype (dtype or TCM_F32), rows ldo >= N elements apart
+ * Elements enter the products as they are, and sums are fp32; scales multiply fp32 sums
+ * of a group.  The result is rounded once.  With TCM_U4 the products with q and with zero are
+ * summed apart and subtracted, so errors go by scale * (q + zero): the result r
+ * satisfies |r - exact| <= u sum_k |x_k| scale (q + zero) (E2M1: |x_k w_k|), u = 2^-17 for K <= 16384
+ * and 2^-12 beyond, plus the rounding; a row of X with a value that is not finite gives NaN there.  Rows of X do not
+ * reach each other's results.  The weights are read once for each 64 rows.  K a multiple of 32, at most 2^20; ldx a multiple of 8 and at
+ * most 2^21; X and W 16-byte aligned, scales and Out by their element.  Out overlaps no input.
+ */
+tcm_status tcm_gemm_w4(const void* X, int64_t ldx, const void* W, const void* scales,
+                       const void* zeros, void* Out, int64_t ldo, int64_t M, int64_t N, int64_t K,
+                       int64_t group, tcm_dtype elem, tcm_dtype dtype, tcm_dtype out_dtype,
+                       void* stream);
+
+/*
+ * Attention of several new tokens per sequence, a tree of drafts or a chain of
+ * tokens, over a paged cache that holds their keys and values already.  The
+ * tokens starts[b] .. starts[b + 1] - 1 (rows of q and out) are sequence b's,
+ * m of them: its last m keys, in order; c = max(0, lengths[b] - m) keys are
+ * before them, the context.  Token i of a sequence, query head h (key-value head
+ * h / (Hq / Hk)):
+ *   out = sum_j p_j v_j,  p = softmax_j(scale * q . k_j)  over its keys j:
+ *   tree NULL   a chain: the keys j <= c + i; with a window, those j > c + i - window
+ *   tree        T rows of tree_words 64-bit words: of its sequence's tokens those
+ *               whose bit is set (token x: bit x % 64 of word x / 64; bits from m on
+ *               mean nothing; its own bit is one of them), and the context; with a
+ *               window, of the context the keys j > c + d - 1 - window, d the number of its
+ *               bits (the token is d - 1 places below the first one of its path)
+ * Keys at lengths[b] and beyond do not exist, nor those in holes of the table.
+ *   q, out   views of T tokens x Hq heads x D; out may be q
+ *   starts   B + 1 int32, not negative, that do not fall (tokens from T on have no rows);
+ *            rows of no sequence are left as they were
+ *   max_nodes  an upper bound of m: of a sequence with more, the tokens from max_nodes on
+ *            are left as they were
+ *   lse      NULL, or T x Hq fp32 (dense): log sum_j exp(scale * q . k_j)
+ * block_table, lengths (the drafted tokens included), max_len, scale, window and the
+ * cache as in tcm_paged_attention, and so are precision and the result of a row without keys.
+ * With a tree tree_words * 64 >= max_nodes (TCM_ERR_INVALID_SHAPE), and tree 8-byte aligned.
+ * T and max_nodes * Hq / Hk at most 2^30, B and Hq at most 65535.
+ */
+tcm_status tcm_paged_tree_attention(const tcm_heads* q, const tcm_cache* cache,
+                                    const int32_t* block_table, int64_t table_stride,
+                                    const int32_t* lengths, int64_t max_len,
+                                    const int32_t* starts, int64_t max_nodes, const uint64_t* tree,
+                                    int64_t tree_words, const tcm_heads* out, float* lse, int64_t T,
+                                    int64_t B, int64_t Hq, int64_t Hk, int64_t D, float scale,
+                                    int64_t window, tcm_dtype dtype, void* workspace,
+                                    int64_t workspace_bytes, void* stream);
+/* (enough also for smaller B, max_nodes and max_len, for every T and for every window) */
+tcm_status tcm_paged_tree_attention_workspace(int64_t B, int64_t Hq, int64_t Hk, int64_t D,
+                                              int64_t max_nodes, int64_t max_len, int64_t* bytes);
 
 /* Static, human-readable name of a status code, the counterpart of the error
  * string lookup of "API Card: Blackwell Pipeline (tcgen05)", Host side.

@@ -30,6 +30,15 @@ The layer around the products (``layer.py``, the same library):
     qk_norm_rope_bwd(dq_out, dk_out, q, k, ...)            its gradients
     paged_attention(q, k_cache, v_cache, ...)              one new token per sequence
     rope_frequencies(rot_dim, base, scaling, ...)          inv_freq and factor
+
+A step that drafts several tokens at once (``step.py``, the same library):
+
+    cache_plan(lengths, change, block_table, ...)          pages, slots and positions of new tokens
+    add_rms_norm(x, weight, residual, ...)                 residual sum and norm
+    add_rms_norm_mx_fp8(x, weight, residual, ...)          the same as MXFP8, for gemm_mx_fp8
+    add_rms_norm_bwd(dout, h, weight, ...)                 its gradients
+    gemm_w4(x, w, scales, zeros, ...)                      few rows times 4-bit weights
+    paged_tree_attention(q, k_cache, v_cache, ...)         a tree or chain of new tokens per sequence
 """
 from __future__ import annotations
 
@@ -39,10 +48,12 @@ import threading
 
 __all__ = ["gemm", "gemm_tn", "gemm_tn_ex", "batched_gemm_tn", "gemm_mx_fp8", "gemm_mx_fp4",
            "gemm_mx_fp6", "gemm_nvfp4", "gemm_mx", "order_ld", "plan", "lib", "TcmError",
-           "LIB_PATH", "F16", "BF16", "F32", "E4M3", "E8M0", "E2M1", "E2M3", "E3M2", "ROW_MAJOR",
+           "LIB_PATH", "F16", "BF16", "F32", "E4M3", "E8M0", "E2M1", "E2M3", "E3M2", "U4", "ROW_MAJOR",
            "COL_MAJOR", "OPS", "lora_gemm_tn", "lora_workspace", "qk_norm_rope", "qk_norm_rope_cache",
            "qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace", "paged_attention",
-           "paged_attention_workspace", "rope_frequencies"]
+           "paged_attention_workspace", "rope_frequencies", "cache_plan", "add_rms_norm",
+           "add_rms_norm_mx_fp8", "add_rms_norm_bwd", "add_rms_norm_bwd_workspace", "gemm_w4",
+           "paged_tree_attention", "paged_tree_attention_workspace"]
 
 # TCM_LIBRARY names another build of the same library (the host-sanitizer
 # build of `python -m tensor_core_matrix_amd.build --sanitize`); by default
@@ -51,7 +62,7 @@ LIB_PATH = os.environ.get("TCM_LIBRARY") or os.path.join(
     os.path.dirname(os.path.abspath(__file__)), "libtcm.so")
 
 # tcm_dtype codes
-F16, BF16, F32, E4M3, E8M0, E2M1, E2M3, E3M2 = 0, 1, 2, 3, 4, 5, 6, 7
+F16, BF16, F32, E4M3, E8M0, E2M1, E2M3, E3M2, U4 = 0, 1, 2, 3, 4, 5, 6, 7, 8
 # tcm_order codes
 ROW_MAJOR, COL_MAJOR = 0, 1
 # tcm_op codes
@@ -103,7 +114,9 @@ EXPORTS = ("tcm_gemm", "tcm_gemm_tn", "tcm_gemm_tn_ex", "tcm_batched_gemm_tn", "
            "tcm_gemm_mx_fp4", "tcm_gemm_mx_fp6", "tcm_gemm_mx", "tcm_gemm_nvfp4", "tcm_plan_gemm",
            "tcm_status_string", "tcm_lora_gemm_tn", "tcm_lora_workspace", "tcm_qk_norm_rope",
            "tcm_qk_norm_rope_cache", "tcm_qk_norm_rope_bwd", "tcm_qk_norm_rope_bwd_workspace",
-           "tcm_paged_attention", "tcm_paged_attention_workspace")
+           "tcm_paged_attention", "tcm_paged_attention_workspace", "tcm_cache_plan", "tcm_add_rms_norm",
+           "tcm_add_rms_norm_mx_fp8", "tcm_add_rms_norm_bwd", "tcm_add_rms_norm_bwd_workspace",
+           "tcm_gemm_w4", "tcm_paged_tree_attention", "tcm_paged_tree_attention_workspace")
 
 
 def lib() -> ctypes.CDLL:
@@ -144,15 +157,24 @@ def lib() -> ctypes.CDLL:
             L.tcm_paged_attention.argtypes = [hd, ca, vp, i64, vp, i64, hd, vp, i64, i64, i64, i64,
                                               cf, i64, ci, vp, i64, vp]
             L.tcm_paged_attention_workspace.argtypes = [i64, i64, i64, i64, i64, pi64]
+            L.tcm_cache_plan.argtypes = [vp, vp, vp, i64, i64, i64, i64, i64, vp, i64, vp, vp, vp, vp, i64,
+                                         vp, vp]
+            L.tcm_add_rms_norm.argtypes = [vp, i64, vp, i64, vp, ci, cf, vp, i64, vp, i64, i64, i64, ci, ci,
+                                           vp]
+            L.tcm_add_rms_norm_mx_fp8.argtypes = [vp, i64, vp, i64, vp, ci, cf, vp, i64, vp, vp, i64, i64,
+                                                  ci, vp]
+            L.tcm_add_rms_norm_bwd.argtypes = [vp, i64, vp, i64, vp, i64, vp, ci, cf, vp, i64, vp, i64, i64,
+                                               ci, vp, i64, vp]
+            L.tcm_add_rms_norm_bwd_workspace.argtypes = [i64, i64, pi64]
+            L.tcm_gemm_w4.argtypes = [vp, i64, vp, vp, vp, vp, i64, i64, i64, i64, i64, ci, ci, ci, vp]
+            L.tcm_paged_tree_attention.argtypes = [hd, ca, vp, i64, vp, i64, vp, i64, vp, i64, hd, vp, i64,
+                                                   i64, i64, i64, i64, cf, i64, ci, vp, i64, vp]
+            L.tcm_paged_tree_attention_workspace.argtypes = [i64, i64, i64, i64, i64, i64, pi64]
             L.tcm_status_string.argtypes = [ci]
             L.tcm_status_string.restype = ctypes.c_char_p
-            for f in ("tcm_gemm", "tcm_gemm_tn", "tcm_gemm_tn_ex", "tcm_batched_gemm_tn", "tcm_gemm_mx_fp8",
-                      "tcm_gemm_mx_fp4", "tcm_gemm_mx_fp6", "tcm_gemm_mx", "tcm_gemm_nvfp4",
-                      "tcm_plan_gemm", "tcm_lora_gemm_tn", "tcm_lora_workspace", "tcm_qk_norm_rope",
-                      "tcm_qk_norm_rope_cache", "tcm_qk_norm_rope_bwd",
-                      "tcm_qk_norm_rope_bwd_workspace", "tcm_paged_attention",
-                      "tcm_paged_attention_workspace"):
-                getattr(L, f).restype = ci
+            for f in EXPORTS:
+                if f != "tcm_status_string":
+                    getattr(L, f).restype = ci
             _lib = L
     return _lib
 
@@ -466,3 +488,5 @@ def plan(M, N, K, dtype=BF16, out_dtype=BF16, batch=1, mx=False, num_cus=256) ->
 from .layer import (lora_gemm_tn, lora_workspace, paged_attention, paged_attention_workspace,  # noqa: E402
                     qk_norm_rope, qk_norm_rope_bwd, qk_norm_rope_bwd_workspace, qk_norm_rope_cache,
                     rope_frequencies)
+from .step import (add_rms_norm, add_rms_norm_bwd, add_rms_norm_bwd_workspace, add_rms_norm_mx_fp8,  # noqa: E402
+                   cache_plan, gemm_w4, paged_tree_attention, paged_tree_attention_workspace)

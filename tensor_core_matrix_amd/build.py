@@ -39,7 +39,8 @@ ARCH = "gfx950"
 SOURCES = ["tcm_api.cpp", "gemm_tn.hip", "gemm_mx.hip", "gemm_mx6.hip", "gemm_nv4.hip", "gemm_epi.hip",
            "gemm_mn_a.hip", "gemm_mn_b.hip", "gemm_mn_ab.hip", "gemm_mx_ld.hip", "gemm_mx_mn_a.hip",
            "gemm_mx_mn_b.hip", "gemm_mx_mn_ab.hip", "layer_api.cpp", "lora.hip", "rope.hip",
-           "paged_attn.hip"]
+           "paged_attn.hip", "step_api.cpp", "norm.hip", "cache_plan.hip", "gemm_w4.hip",
+           "tree_attn_bf16.hip", "tree_attn_f16.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-I", os.path.join(ROOT, "include")]

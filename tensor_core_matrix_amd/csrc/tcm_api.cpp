@@ -95,7 +95,8 @@ int elem_bytes(tcm_dtype d) {
     case TCM_E8M0: return 1;
     case TCM_E2M1:
     case TCM_E2M3:
-    case TCM_E3M2: return 0;  // packed below a byte
+    case TCM_E3M2:
+    case TCM_U4: return 0;  // packed below a byte
     }
     return 0;
 }
