@@ -90,7 +90,8 @@ struct TreeArgs {
     float* pml;  // and as many pairs (maximum in base 2, sum)
     int32_t T, B, Hq, Hk, G, D;
     int32_t pages, page_size;
-    int32_t page_shift;  // log2 of page_size where it is a power of two, else -1
+    uint32_t page_magic;  // n / page_size = n * page_magic >> page_shift for n < 2^31
+    int32_t page_shift;
     int32_t max_len, max_nodes, window;
     int32_t chunk, splits;
     int32_t blocks;  // blocks of rows of one sequence and key-value head

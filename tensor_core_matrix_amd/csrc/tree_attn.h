@@ -11,15 +11,15 @@
 // lane (as two parts of 8 or 11 bits): the 8 inner positions of lane group g there are keys
 // 4 g + j of a tile's first 16 and of its second.
 //
-// Keys and values go from memory straight into a ring of LDS stages of 32 keys, in rows whose
+// Keys and values go from memory straight into one of two LDS stages, a tile ahead, in rows whose
 // 16-byte pieces are exchanged so that operand reads meet all banks; values are read transposed.
 // Pieces past a head's end, keys past the sequence's, and holes are offsets out of a buffer's
 // range: they arrive as zeros.  (Pages whose size 16 does not divide go through registers, since
 // a copy has one base address for its keys.)
 //
-// WR waves share a stage and take 16 RB rows each; WK groups of WR waves take every WK-th tile
-// and meet in LDS at the end.  16 rows or fewer: 1 x 4, each wave a ring of its own and no
-// barrier; more: 4 x 1, one barrier a tile.  With more than one chunk of keys tree_join_kernel joins
+// WR waves share the stages and take 16 RB rows each; WK groups of WR waves take every WK-th tile
+// and meet in LDS at the end.  16 rows or fewer: 1 x 4 and tiles of 32 keys, each wave stages of its own and no
+// barrier; more: 4 x 1 and tiles of 64, one barrier a tile.  With more than one chunk of keys tree_join_kernel joins
 // the parts.
 //
 // Which keys a row sees is a word of 32 bits a tile, made for tiles that need it: those that reach
@@ -97,33 +97,34 @@ struct TreeShape {
     static constexpr int WR = WR_, RB = RB_;
     static constexpr int ES = E4M3 ? 1 : 2;
     static constexpr int KB = DP * ES;            // bytes of a key
-    static constexpr int TILE = 2 * 32 * KB;      // of 32 keys and values
-    // groups of waves over the keys; four rings of two stages fit in LDS up to 256 bytes a key
+    static constexpr int NT = WR > 1 ? 2 : 1;     // 32 keys of a tile
+    static constexpr int KT = 32 * NT;            // keys of a tile
+    static constexpr int STAGE = 2 * KT * KB;     // its keys and values
+    // groups of waves over the keys; four pairs of stages fit in LDS up to 256 bytes a key
     static constexpr int WK = WR > 1 ? 1 : KB <= 256 ? 4 : 2;
-    static constexpr int NS = WR > 1 ? 3 : 2;     // stages of a ring
     static constexpr int WAVES = WR * WK;
     static constexpr int ROWS = 16 * WR * RB;     // of a workgroup
-    static constexpr int RING = WK * NS * TILE;
     static constexpr int MEET = WK > 1 ? WK * 16 * (DP + 4) * 4 : 0;
-    static constexpr int LDS = RING > MEET ? RING : MEET;
+    static constexpr int LDS = 2 * WK * STAGE > MEET ? 2 * WK * STAGE : MEET;
 };
 
-// DP: D rounded up to 64, 128 or 256.  ALIGNED: page_size is a multiple of 16, so the 16 keys of a
-// half tile lie in one page.
+// DP: D rounded up to 64, 128 or 256.  ALIGNED: page_size is a multiple of 16, so 16 keys from a multiple
+// of 16 on lie in one page.
 template <class T, int DP, bool E4M3, bool ALIGNED, int WR, int RB>
 __global__ __launch_bounds__((TreeShape<DP, E4M3, WR, RB>::WAVES * 64), (TreeShape<DP, E4M3, WR, RB>::LDS > 72 * 1024 ? 1 : 2)) void tree_kernel(TreeArgs p) {
     typedef TreeShape<DP, E4M3, WR, RB> S;
     typedef Half16<T> H;
     typedef typename H::x8 x8;
-    constexpr int ES = S::ES, KB = S::KB, WK = S::WK, NS = S::NS;
+    constexpr int ES = S::ES, KB = S::KB, WK = S::WK, NT = S::NT, KT = S::KT;
     constexpr int STEPS = DP / 32;     // products of 32 over the head
     constexpr int VE = DP / 16;        // products of 16 elements
     constexpr int KL = KB / 16;        // lanes that copy a key,
     constexpr int KN = 64 / KL;        // keys of one copy,
-    constexpr int KI = 32 / KN;        // and copies of a tile's keys (and of its values)
-    constexpr int NL = 2 * KI / WR;    // a wave's part of both
+    constexpr int HALF = 16 / KN;      // and copies of 16 keys (or values)
+    // A wave's part of a tile: 16 keys and their values NH times
+    constexpr int NH = 2 * NT / WR;
+    static_assert(NH * WR == 2 * NT, "a wave's copies");
     __shared__ __attribute__((aligned(1024))) char lds[S::LDS];
-    __shared__ float pr_[S::WAVES][32][16];
     __shared__ float lm_[RB][WK][16], ll_[RB][WK][16];
 
     const int lane = threadIdx.x & 63;
@@ -153,9 +154,140 @@ __global__ __launch_bounds__((TreeShape<DP, E4M3, WR, RB>::WAVES * 64), (TreeSha
         tok[i] = row / p.G;
         head[i] = hk * p.G + row - tok[i] * p.G;
     }
+
+    // ---- keys and values into LDS ---------------------------------------------------
+    // A key's 16-byte piece c lies in LDS at c ^ swz(key), so that the 16 keys of an operand read
+    // meet different banks; swz goes by the key's number within 16.
+    constexpr int SH = KL >= 16 ? 0 : KL == 8 ? 1 : 2;
+    auto swz = [](int key) { return (key >> SH) & ((KL < 16 ? KL : 16) - 1); };
+    char* const stages = lds + wk * 2 * S::STAGE;  // a stage: KT keys, KT values
+    const int kc = lane % KL, kr = lane / KL;
+    const int32_t* const trow = p.table + b * p.table_stride;
+    const char* const kh = p.kc + hk * p.k_head;
+    const char* const vh = p.vc + hk * p.v_head;
+    auto page_of = [&](int key) { return (int)((uint64_t)(uint32_t)key * p.page_magic >> p.page_shift); };
+    // ALIGNED, shared stages: whether the page of 16 keys of a stage is one
+    __shared__ uint32_t there_[2][4];
+    struct Tile {
+        int key0;
+        int page[NH];       // ALIGNED: of the 16 keys that the wave copies; else [0] of key l % KT of lane l
+        int entry[NH];      // and their numbers in the table's row
+        uint32_t good[NT];  // the keys that can be used at all (ALIGNED, shared stages: but for their pages)
+    };
+    auto look = [&](int key0) {
+        Tile t;
+        t.key0 = key0;
+        if constexpr (ALIGNED) {
+#pragma unroll
+            for (int y = 0; y < NH; ++y) {
+                const int key = key0 + 16 * (WR > 1 ? wr : y);
+                t.entry[y] = page_of(key);
+                t.page[y] = key < end ? trow[t.entry[y]] : -1;
+            }
+        } else {
+            const int key = key0 + (lane & (KT - 1));
+            t.entry[0] = page_of(key);
+            t.page[0] = key >= rg.lo && key < end ? trow[t.entry[0]] : -1;
+        }
+        return t;
+    };
+    // ALIGNED: a lane's offsets from the first of 16 keys (16 token strides are less than 2^31 bytes)
+    uint32_t koff[HALF], voff[HALF];
+#pragma unroll
+    for (int q = 0; q < HALF; ++q) {
+        const int key = q * KN + kr, piece = kc ^ swz(key);
+        const bool in = 16 * piece < p.D * ES;
+        koff[q] = in ? key * (uint32_t)p.k_tok + piece * 16 : kOutOfRange;
+        voff[q] = in ? key * (uint32_t)p.v_tok + piece * 16 : kOutOfRange;
+    }
+    u32x4_t held[ALIGNED ? 1 : 2 * NH * HALF];
+    auto issue = [&](Tile& t, int stage) {
+        char* const to = stages + stage * S::STAGE;
+        if constexpr (ALIGNED) {
+            const bool whole = t.key0 >= rg.lo && t.key0 + KT <= end;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) t.good[n] = whole ? ~0u : bits_from(rg.lo - t.key0 - 32 * n) & ~bits_from(end - t.key0 - 32 * n);
+#pragma unroll
+            for (int y = 0; y < NH; ++y) {
+                const int h = WR > 1 ? wr : y;
+                const int key = t.key0 + 16 * h;
+                const uint32_t found = __builtin_amdgcn_readfirstlane(t.page[y]);
+                const bool is = found < (uint32_t)p.pages;
+                if constexpr (WR > 1) there_[stage][wr] = is ? 0xffffu << (wr & 1) * 16 : 0u;
+                else if (!is) t.good[0] &= h ? 0x0000ffffu : 0xffff0000u;
+                const uint32_t size = is ? kOutOfRange : 0u, page = is ? found : 0;
+                const uint32_t at = key - t.entry[y] * p.page_size;
+                const __amdgpu_buffer_rsrc_t rk = make_rsrc(kh + (page * (uint64_t)p.k_page + at * (uint64_t)p.k_tok), size);
+                const __amdgpu_buffer_rsrc_t rv = make_rsrc(vh + (page * (uint64_t)p.v_page + at * (uint64_t)p.v_tok), size);
+                char* const dk = to + h * 16 * KB;
+                char* const dv = dk + KT * KB;
+                if (whole) {
+#pragma unroll
+                    for (int q = 0; q < HALF; ++q) copy16_to_lds_asm(rk, dk + q * 1024, koff[q]);
+#pragma unroll
+                    for (int q = 0; q < HALF; ++q) copy16_to_lds_asm(rv, dv + q * 1024, voff[q]);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < HALF; ++q) {
+                        const int k = key + q * KN + kr;
+                        const bool in = k >= rg.lo && k < end;
+                        copy16_to_lds_asm(rk, dk + q * 1024, in ? koff[q] : kOutOfRange);
+                        copy16_to_lds_asm(rv, dv + q * 1024, in ? voff[q] : kOutOfRange);
+                    }
+                }
+            }
+        } else {
+            const bool ok = (uint32_t)t.page[0] < (uint32_t)p.pages;
+            if (!ok) t.page[0] = -1;
+            const uint64_t all = __ballot(ok);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) t.good[n] = (uint32_t)(all >> 32 * n);
+#pragma unroll
+            for (int y = 0; y < NH; ++y)
+#pragma unroll
+                for (int q = 0; q < HALF; ++q) {
+                    const int key = (WR > 1 ? wr : y) * 16 + q * KN + kr, piece = kc ^ swz(key & 15);
+                    const int page = __shfl(t.page[0], key), at = t.key0 + key - __shfl(t.entry[0], key) * p.page_size;
+                    u32x4_t& k = held[2 * (y * HALF + q)];
+                    u32x4_t& v = held[2 * (y * HALF + q) + 1];
+                    k = v = (u32x4_t){};
+                    if (page >= 0 && 16 * piece < p.D * ES) {
+                        k = *(const u32x4_t*)(kh + page * p.k_page + at * p.k_tok + piece * 16);
+                        v = *(const u32x4_t*)(vh + page * p.v_page + at * p.v_tok + piece * 16);
+                    }
+                }
+        }
+    };
+    // what issue() left in registers
+    auto settle = [&](int stage) {
+        if constexpr (!ALIGNED) {
+#pragma unroll
+            for (int y = 0; y < NH; ++y)
+#pragma unroll
+                for (int q = 0; q < HALF; ++q) {
+                    char* const to = stages + stage * S::STAGE + (WR > 1 ? wr : y) * 16 * KB + q * 1024 + lane * 16;
+                    *(u32x4_t*)to = held[2 * (y * HALF + q)];
+                    *(u32x4_t*)(to + KT * KB) = held[2 * (y * HALF + q) + 1];
+                }
+        }
+    };
+
+    // ---- the tiles of this group of waves ----------------------------------------------
+    // Tile r + 1 is asked for while tile r is computed; its pages were looked up a tile before, by loads that
+    // the wait for tile r's copies covers.  (A scalar load's wait would be the next one for an operand from
+    // LDS, since both have one counter.)
+    constexpr int ROUND = KT * WK;
+    const int first = start + KT * wk;
+    const int tiles = first < end ? (end - first + ROUND - 1) / ROUND : 0;
+    Tile tile = look(first);
+    if (tiles > 0) issue(tile, 0);
+    Tile next = look(first + ROUND);
+
     // Q as the second operand: lane l holds row l % 16 and 8 elements of each step.  Elements of step
     // s: 32 s + 8 g .. + 7; for E4M3 keys, whose 16-byte pieces cover two steps,
-    // 64 (s / 2) + 16 g + 8 (s % 2) .. + 7.
+    // 64 (s / 2) + 16 g + 8 (s % 2) .. + 7.  A negative scale is q's sign (a scale of 0 the least there is:
+    // masked scores are -infinity times it).
+    const float scale = fmaxf(fabsf(p.scale_log2), 0x1p-126f);
     x8 qf[RB][STEPS];
 #pragma unroll
     for (int i = 0; i < RB; ++i) {
@@ -182,123 +314,18 @@ __global__ __launch_bounds__((TreeShape<DP, E4M3, WR, RB>::WAVES * 64), (TreeSha
             }
         }
     }
-
-    // ---- keys and values into LDS ---------------------------------------------------
-    // A key's 16-byte piece c lies in LDS at c ^ swz(key), so that the 16 keys of an operand read
-    // meet different banks; swz goes by the key's number within 16.
-    constexpr int SH = KL >= 16 ? 0 : KL == 8 ? 1 : 2;
-    auto swz = [](int key) { return (key >> SH) & ((KL < 16 ? KL : 16) - 1); };
-    char* const ring = lds + wk * NS * S::TILE;  // a stage: 32 keys, 32 values
-    const int kc = lane % KL, kr = lane / KL;
-    const int32_t* const trow = p.table + b * p.table_stride;
-    const char* const kh = p.kc + hk * p.k_head;
-    const char* const vh = p.vc + hk * p.v_head;
-    auto page_of = [&](int key, int& at) {
-        const int i = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
-        at = key - i * p.page_size;
-        return i;
-    };
-    // Copy q of a wave (0 .. NL - 1): with shared stages, half of the waves copy keys and half
-    // values.
-    auto is_value = [&](int q) { return WR > 1 ? wr >= WR / 2 : q >= KI; };
-    auto piece_of = [&](int q) { return WR > 1 ? (wr % (WR / 2)) * NL + q : q % KI; };
-    struct Tile {  // its pages (ALIGNED: of each half; else of key l % 32 of lane l), and its keys
-        int page[2], at[2];
-        int key0;
-        uint32_t good;  // the keys that can be used at all
-    };
-    auto look = [&](int key0) {
-        Tile t;
-        t.key0 = key0;
-        if constexpr (ALIGNED) {
+    // (used here, so that the compiler's wait for q is not in the loop, where it would be one for the copies)
+    const uint32_t flip = p.scale_log2 < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int key = key0 + 16 * h;
-                const int i = page_of(key, t.at[h]);
-                t.page[h] = key < end ? scalar_int(trow + i) : -1;
-            }
-        } else {
-            const int key = key0 + (lane & 31);
-            const int i = page_of(key, t.at[0]);
-            t.page[0] = key >= rg.lo && key < end ? trow[i] : -1;
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            qf[i][s] = __builtin_bit_cast(x8, __builtin_bit_cast(u32x4_t, qf[i][s]) ^ flip);
+            asm volatile("" : "+v"(qf[i][s]));
         }
-        return t;
-    };
-    // ALIGNED: a lane's offsets from the first of 16 keys (16 token strides are less than 2^31 bytes)
-    uint32_t voff[ALIGNED ? (WR > 1 ? NL : 2 * (16 / KN > 0 ? 16 / KN : 1)) : 1];
-    if constexpr (ALIGNED) {
-#pragma unroll
-        for (int q = 0; q < (int)(sizeof(voff) / 4); ++q) {
-            // (WR == 1: of a half's keys, then of its values)
-            constexpr int HALF = 16 / KN;
-            const bool val = WR > 1 ? is_value(0) : q >= HALF;
-            const int key = (WR > 1 ? piece_of(q) % HALF : q % HALF) * KN + kr;
-            const int piece = kc ^ swz(key);
-            voff[q] = 16 * piece < p.D * ES ? key * (uint32_t)(val ? p.v_tok : p.k_tok) + piece * 16 : kOutOfRange;
-        }
-    }
-    u32x4_t held[ALIGNED ? 1 : NL];
-    auto issue = [&](Tile& t, int stage) {
-        char* const to = ring + stage * S::TILE;
-        if constexpr (ALIGNED) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                if ((uint32_t)t.page[h] >= (uint32_t)p.pages) t.page[h] = -1;
-            t.good = ((t.page[0] >= 0 ? 0xffffu : 0u) | (t.page[1] >= 0 ? 0xffff0000u : 0u)) & bits_from(rg.lo - t.key0) &
-                     ~bits_from(end - t.key0);
-            const bool whole = t.key0 >= rg.lo && t.key0 + 32 <= end;
-            constexpr int HALF = 16 / KN;
-            __amdgpu_buffer_rsrc_t rk[2], rv[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t size = t.page[h] >= 0 ? kOutOfRange : 0u;
-                const int64_t pg = max(t.page[h], 0);
-                rk[h] = make_rsrc(kh + pg * p.k_page + t.at[h] * p.k_tok, size);
-                rv[h] = make_rsrc(vh + pg * p.v_page + t.at[h] * p.v_tok, size);
-            }
-#pragma unroll
-            for (int q = 0; q < NL; ++q) {
-                const int i = piece_of(q);
-                uint32_t off;
-                if constexpr (WR > 1) off = voff[q];
-                else off = voff[(q >= KI ? HALF : 0) + q % HALF];
-                if (!whole) {
-                    const int key = t.key0 + i * KN + kr;
-                    off = key >= rg.lo && key < end ? off : kOutOfRange;
-                }
-                char* const dst = to + (is_value(q) ? 32 * KB : 0) + i * 1024;
-                // (the half is known to the compiler or, with shared stages, to the wave)
-                const bool second = i >= KI / 2;
-                if (is_value(q)) copy16_to_lds_asm(second ? rv[1] : rv[0], dst, off);
-                else copy16_to_lds_asm(second ? rk[1] : rk[0], dst, off);
-            }
-        } else {
-            const bool ok = (uint32_t)t.page[0] < (uint32_t)p.pages;
-            if (!ok) t.page[0] = -1;
-            t.good = (uint32_t)__ballot(ok);
-#pragma unroll
-            for (int q = 0; q < NL; ++q) {
-                const int key = piece_of(q) * KN + kr, piece = kc ^ swz(key);
-                const int page = __shfl(t.page[0], key), at = __shfl(t.at[0], key);
-                const char* row = is_value(q) ? vh + max(page, 0) * p.v_page + at * p.v_tok
-                                              : kh + max(page, 0) * p.k_page + at * p.k_tok;
-                held[q] = (u32x4_t){};
-                if (page >= 0 && 16 * piece < p.D * ES) held[q] = *(const u32x4_t*)(row + piece * 16);
-            }
-        }
-    };
-    // what issue() left in registers
-    auto settle = [&](int stage) {
-        if constexpr (!ALIGNED) {
-            char* const to = ring + stage * S::TILE;
-#pragma unroll
-            for (int q = 0; q < NL; ++q)
-                *(u32x4_t*)(to + (is_value(q) ? 32 * KB : 0) + piece_of(q) * 1024 + lane * 16) = held[q];
-        }
-    };
 
     f32x4_t o[RB][VE];
-    float mx[RB], sum[RB];
+    float mx[RB], sum[RB];  // the largest score, unscaled, and the sum of exponentials
 #pragma unroll
     for (int i = 0; i < RB; ++i) {
 #pragma unroll
@@ -307,20 +334,96 @@ __global__ __launch_bounds__((TreeShape<DP, E4M3, WR, RB>::WAVES * 64), (TreeSha
         sum[i] = 0.0f;
     }
 
-    auto compute = [&](const char* at, uint32_t good, int key0) {
-        const char* const kt = at;
-        const char* const vt = at + 32 * KB;
-        const bool plain = good == ~0u && key0 >= rg.sure && key0 + 32 <= rg.safe;
-        f32x4_t s[RB][2];
+    // Which of the keys 32 n .. of a tile row i of this lane sees.  (Lanes' numbers by way of a register that the compiler
+    // does not look through: what the rare tiles need is not to be kept over the others.)
+    auto row_sees = [&](int i, int n, const uint32_t* good, int key0) {
+        const int x0 = key0 + 32 * n - rg.context;  // the first key's number among the tokens
+        uint32_t bits;
+        if (!p.tree) {
+            bits = ~bits_from(tok[i] - x0 + 1);
+        } else {
+            const uint32_t* words = p.tree + (int64_t)(rg.row0 + tok[i]) * p.tree_words;
+            const int w = x0 >> 5, sh = x0 & 31;
+            const uint32_t w0 = w >= 0 && w < p.tree_words ? words[w] : 0u;
+            const uint32_t w1 = w >= -1 && w + 1 < p.tree_words ? words[w + 1] : 0u;
+            bits = __builtin_amdgcn_alignbit(w1, w0, sh) | ~bits_from(-x0);
+        }
+        return bits & good[n] & bits_from(low[i] - key0 - 32 * n);
+    };
+    // A tile that not every row sees whole: values that are not finite are added to the rows that see their keys
+    // (infinities and NaN: a probability, which is positive, would not change them), and become zeros.
+    auto set_apart = [&](int stage, const uint32_t* good, int key0) {
+        char* const vt = stages + stage * S::STAGE + KT * KB;
+        int own_lane = lane;
+        asm volatile("" : "+v"(own_lane));
+        bool strange = false;
+        for (int i = own_lane * 16; i < KT * KB; i += 1024) {
+            const u32x4_t v = *(const u32x4_t*)(vt + i);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+            for (int y = 0; y < 4; ++y) strange = strange || not_finite<T, E4M3>(v[y]);
+        }
+        if (!__any(strange)) return;  // (the waves that share the stage agree: they look at the same values)
+        if (rows > 0)
 #pragma unroll
-            for (int i = 0; i < RB; ++i) s[i][h] = (f32x4_t){};
-            const char* row = kt + (16 * h + r16) * KB;
-            const int sw = swz(r16);
+            for (int i = 0; i < RB; ++i)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const uint32_t sees = row_sees(i, n, good, key0);
+                    for (int k = 0; k < 32; ++k) {
+                        const char* row = vt + (32 * n + k) * KB;
+#pragma unroll
+                        for (int m = 0; m < VE; ++m) {
+                            const int d = 16 * m + 4 * (own_lane >> 4);
+                            const char* at = row + ((d * ES / 16) ^ swz(k & 15)) * 16 + d * ES % 16;
+                            uint32_t u[2];
+                            if constexpr (E4M3) {
+                                const uint32_t w = *(const uint32_t*)at;
+                                u[0] = H::from_fp8(w, false);
+                                u[1] = H::from_fp8(w, true);
+                            } else {
+                                u[0] = *(const uint32_t*)at;
+                                u[1] = *(const uint32_t*)(at + 4);
+                            }
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) {
+                                const float z = (float)__builtin_bit_cast(T, (uint16_t)(u[y >> 1] >> 16 * (y & 1)));
+                                o[i][m][y] += (sees >> k & 1) && !(fabsf(z) < __builtin_inff()) ? z : 0.0f;
+                            }
+                        }
+                    }
+                }
+        if constexpr (WR > 1) barrier_lds();
+        else wave_lds_exchange();
+        for (int i = (wr * 64 + own_lane) * 4; i < KT * KB; i += WR * 256) {
+            uint32_t v = *(const uint32_t*)(vt + i);
             if constexpr (E4M3) {
 #pragma unroll
-                for (int st = 0; st < STEPS; st += 2) {
+                for (int y = 0; y < 4; ++y) v = (v >> 8 * y & 0x7f) == 0x7f ? v & ~(0xffu << 8 * y) : v;
+            } else {
+                v = not_finite<T, E4M3>(v & 0xffffu) ? v & 0xffff0000u : v;
+                v = not_finite<T, E4M3>(v & 0xffff0000u) ? v & 0xffffu : v;
+            }
+            *(uint32_t*)(vt + i) = v;
+        }
+        if constexpr (WR > 1) barrier_lds();
+        else wave_lds_exchange();
+    };
+    auto products = [&](int stage, bool plain, const uint32_t* good, int key0) {
+        const char* const kt = stages + stage * S::STAGE;
+        const char* const vt = kt + KT * KB;
+        float x[RB][8 * NT];
+        f32x4_t s[RB][2 * NT];
+#pragma unroll
+        for (int i = 0; i < RB; ++i)
+#pragma unroll
+            for (int h = 0; h < 2 * NT; ++h) s[i][h] = (f32x4_t){};
+#pragma unroll
+        for (int st = 0; st < STEPS; st += E4M3 ? 2 : 1)
+#pragma unroll
+            for (int h = 0; h < 2 * NT; ++h) {
+                const char* row = kt + (16 * h + r16) * KB;
+                const int sw = swz(r16);
+                if constexpr (E4M3) {
                     const i32x4_t w4 = *(const i32x4_t*)(row + ((2 * st + g4) ^ sw) * 16);
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
@@ -332,61 +435,70 @@ __global__ __launch_bounds__((TreeShape<DP, E4M3, WR, RB>::WAVES * 64), (TreeSha
 #pragma unroll
                         for (int i = 0; i < RB; ++i) s[i][h] = H::mma(__builtin_bit_cast(x8, u), qf[i][st + y], s[i][h]);
                     }
-                }
-            } else {
-#pragma unroll
-                for (int st = 0; st < STEPS; ++st) {
+                } else {
                     const x8 kf = *(const x8*)(row + ((4 * st + g4) ^ sw) * 16);
 #pragma unroll
                     for (int i = 0; i < RB; ++i) s[i][h] = H::mma(kf, qf[i][st], s[i][h]);
                 }
             }
-        }
-        float x[RB][8];
 #pragma unroll
         for (int i = 0; i < RB; ++i)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[i][j] = s[i][j >> 2][j & 3] * p.scale_log2;
-        // the keys of inner positions 0..7 of this lane in the second product
-        auto vkey = [&](int j) { return (j < 4 ? 0 : 16) + 4 * g4 + (j & 3); };
-        uint32_t seen[RB];
-        bool strange = false;  // a value that is not finite
+            for (int j = 0; j < 8 * NT; ++j) x[i][j] = s[i][j >> 2][j & 3];
         if (!plain) {
             asm volatile("");  // (a branch: as selects it would run for every tile)
-            const int x0 = key0 - rg.context;  // the number of key0 among the tokens
 #pragma unroll
-            for (int i = 0; i < RB; ++i) {
-                uint32_t bits;
-                if (!p.tree) {
-                    bits = ~bits_from(tok[i] - x0 + 1);
-                } else {
-                    const uint32_t* words = p.tree + (int64_t)(rg.row0 + tok[i]) * p.tree_words;
-                    const int w = x0 >> 5, sh = x0 & 31;
-                    const uint32_t w0 = w >= 0 && w < p.tree_words ? words[w] : 0u;
-                    const uint32_t w1 = w >= -1 && w + 1 < p.tree_words ? words[w + 1] : 0u;
-                    bits = __builtin_amdgcn_alignbit(w1, w0, sh) | ~bits_from(-x0);
+            for (int i = 0; i < RB; ++i)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const uint32_t sees = row_sees(i, n, good, key0) >> 4 * g4;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[i][8 * n + j] = sees >> ((j < 4 ? 0 : 16) + (j & 3)) & 1 ? x[i][8 * n + j] : kNegInf;
                 }
-                seen[i] = bits & good & bits_from(low[i] - key0);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[i][j] = seen[i] >> vkey(j) & 1 ? x[i][j] : kNegInf;
-            }
-            for (int i = lane * 16; i < 32 * KB; i += 1024) {
-                const u32x4_t v = *(const u32x4_t*)(vt + i);
-#pragma unroll
-                for (int y = 0; y < 4; ++y) strange = strange || not_finite<T, E4M3>(v[y]);
-            }
-            strange = __any(strange);
         }
-        x8 upper[RB], lower[RB];
+        // Values, 16 elements of 8 keys a lane, asked for before the softmax that their products wait for
+        constexpr int VG = RB > 1 || VE < 8 ? 4 : 8;  // products whose values are in registers at once
+        x8 v[VG];
+        auto read_values = [&](int n, int m0) {
+#pragma unroll
+            for (int y = 0; y < VG; ++y) {
+                const int m = m0 + y;
+                if constexpr (E4M3) {
+                    // 8 rows of 16 bytes, row r from lanes 2 r and 2 r + 1
+                    const int r = r16 >> 1, key = (r < 4 ? 0 : 16) + 4 * g4 + (r & 3);
+                    const i32x2_t w = lds_read_tr8(vt + (32 * n + key) * KB + (m ^ swz(key & 15)) * 16 + 8 * (r16 & 1));
+                    v[y] = __builtin_bit_cast(x8, (u32x4_t){H::from_fp8(w[0], false), H::from_fp8(w[0], true),
+                                                            H::from_fp8(w[1], false), H::from_fp8(w[1], true)});
+                } else {
+                    // twice 4 rows of 16 elements, row r from lanes 4 r .. 4 r + 3
+                    const int key = 4 * g4 + (r16 >> 2), c = 2 * m + (r16 >> 1 & 1);
+                    const char* at = vt + (32 * n + key) * KB + (c ^ swz(key)) * 16 + 8 * (r16 & 1);
+                    union {
+                        s16x4_t half[2];
+                        x8 all;
+                    } u;
+                    u.half[0] = lds_read_tr16(at);
+                    u.half[1] = lds_read_tr16(at + 16 * KB);
+                    v[y] = u.all;
+                }
+            }
+        };
+        float top[RB];
+        bool higher = false;
 #pragma unroll
         for (int i = 0; i < RB; ++i) {
-            float top = x[i][0];
+            top[i] = x[i][0];
 #pragma unroll
-            for (int j = 1; j < 8; ++j) top = fmaxf(top, x[i][j]);
-            top = max_over_groups(top);
-            if (__any(top > mx[i])) {
-                const float m2 = fmaxf(mx[i], top);
-                const float f = m2 == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(mx[i] - m2);
+            for (int j = 1; j < 8 * NT; ++j) top[i] = fmaxf(top[i], x[i][j]);
+            top[i] = max_over_groups(top[i]);
+            higher = higher || top[i] > mx[i];
+        }
+        if (__any(higher)) {
+#pragma unroll
+            for (int i = 0; i < RB; ++i) {
+                const float m2 = fmaxf(mx[i], top[i]);
+                // (o may hold infinities: from the least factor on they stay)
+                const float f = mx[i] == kNegInf ? 1.0f : fmaxf(__builtin_amdgcn_exp2f((mx[i] - m2) * scale), 0x1p-126f);
                 mx[i] = m2;
                 sum[i] *= f;
 #pragma unroll
@@ -394,134 +506,73 @@ __global__ __launch_bounds__((TreeShape<DP, E4M3, WR, RB>::WAVES * 64), (TreeSha
 #pragma unroll
                     for (int y = 0; y < 4; ++y) o[i][m][y] *= f;
             }
-            const float m0 = mx[i] == kNegInf ? 0.0f : mx[i];
-            u32x4_t pu, pl;
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-                x[i][j] = __builtin_amdgcn_exp2f(x[i][j] - m0);
-                x[i][j + 1] = __builtin_amdgcn_exp2f(x[i][j + 1] - m0);
-                sum[i] += x[i][j];
-                sum[i] += x[i][j + 1];
-                uint32_t u, l;
-                H::parts(x[i][j], x[i][j + 1], u, l);
-                pu[j / 2] = u;
-                pl[j / 2] = l;
-            }
-            upper[i] = __builtin_bit_cast(x8, pu);
-            lower[i] = __builtin_bit_cast(x8, pl);
         }
-        if (!strange) {
 #pragma unroll
-            for (int m = 0; m < VE; ++m) {
-                x8 v;
-                if constexpr (E4M3) {
-                    // 8 rows of 16 bytes, row r from lanes 2 r and 2 r + 1
-                    const int r = r16 >> 1, key = (r < 4 ? 0 : 16) + 4 * g4 + (r & 3);
-                    const i32x2_t w = lds_read_tr8(vt + key * KB + (m ^ swz(key & 15)) * 16 + 8 * (r16 & 1));
-                    v = __builtin_bit_cast(x8, (u32x4_t){H::from_fp8(w[0], false), H::from_fp8(w[0], true),
-                                                         H::from_fp8(w[1], false), H::from_fp8(w[1], true)});
-                } else {
-                    // twice 4 rows of 16 elements, row r from lanes 4 r .. 4 r + 3
-                    const int key = 4 * g4 + (r16 >> 2), c = 2 * m + (r16 >> 1 & 1);
-                    const char* at = vt + key * KB + (c ^ swz(key)) * 16 + 8 * (r16 & 1);
-                    union {
-                        s16x4_t half[2];
-                        x8 all;
-                    } u;
-                    u.half[0] = lds_read_tr16(at);
-                    u.half[1] = lds_read_tr16(at + 16 * KB);
-                    v = u.all;
-                }
-#pragma unroll
-                for (int i = 0; i < RB; ++i) {
-                    o[i][m] = H::mma(v, upper[i], o[i][m]);
-                    o[i][m] = H::mma(v, lower[i], o[i][m]);
-                }
-            }
-        } else {
-            // key by key, and only for the rows that see it
-            float (*const pr)[16] = pr_[wave];
+        for (int n = 0; n < NT; ++n) {
+            read_values(n, 0);
+            x8 upper[RB], lower[RB];
 #pragma unroll
             for (int i = 0; i < RB; ++i) {
-                wave_lds_exchange();
+                const float m0 = mx[i] == kNegInf ? 0.0f : mx[i] * scale;
+                u32x4_t pu, pl;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) pr[vkey(j)][r16] = x[i][j] * H::kLift;
-                wave_lds_exchange();
-                for (int k = 0; k < 32; ++k) {
-                    const float f = pr[k][r16];
-                    const bool sees = seen[i] >> k & 1;
-#pragma unroll
-                    for (int m = 0; m < VE; ++m) {
-                        const int d = 16 * m + 4 * g4;
-                        const char* at = vt + k * KB + ((d * ES / 16) ^ swz(k & 15)) * 16 + d * ES % 16;
-                        uint32_t u[2];
-                        if constexpr (E4M3) {
-                            const uint32_t w = *(const uint32_t*)at;
-                            u[0] = H::from_fp8(w, false);
-                            u[1] = H::from_fp8(w, true);
-                        } else {
-                            u[0] = *(const uint32_t*)at;
-                            u[1] = *(const uint32_t*)(at + 4);
-                        }
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            const float v = (float)__builtin_bit_cast(T, (uint16_t)(u[y >> 1] >> 16 * (y & 1)));
-                            o[i][m][y] += sees ? f * v : 0.0f;
-                        }
-                    }
+                for (int j = 0; j < 8; j += 2) {
+                    float& e0 = x[i][8 * n + j];
+                    float& e1 = x[i][8 * n + j + 1];
+                    e0 = __builtin_amdgcn_exp2f(fmaf(e0, scale, -m0));
+                    e1 = __builtin_amdgcn_exp2f(fmaf(e1, scale, -m0));
+                    sum[i] += e0;
+                    sum[i] += e1;
+                    uint32_t u, l;
+                    H::parts(e0, e1, u, l);
+                    pu[j / 2] = u;
+                    pl[j / 2] = l;
                 }
+                upper[i] = __builtin_bit_cast(x8, pu);
+                lower[i] = __builtin_bit_cast(x8, pl);
             }
-            wave_lds_exchange();
+#pragma unroll
+            for (int m0 = 0; m0 < VE; m0 += VG) {
+                if (m0 > 0) read_values(n, m0);
+#pragma unroll
+                for (int y = 0; y < VG; ++y)
+#pragma unroll
+                    for (int i = 0; i < RB; ++i) o[i][m0 + y] = H::mma(v[y], upper[i], o[i][m0 + y]);
+#pragma unroll
+                for (int y = 0; y < VG; ++y)
+#pragma unroll
+                    for (int i = 0; i < RB; ++i) o[i][m0 + y] = H::mma(v[y], lower[i], o[i][m0 + y]);
+            }
         }
     };
 
-    // ---- the tiles of this group of waves ----------------------------------------------
-    constexpr int ROUND = 32 * WK;
-    const int first = start + 32 * wk;
-    const int tiles = first < end ? (end - first + ROUND - 1) / ROUND : 0;
-    if constexpr (ALIGNED) {
-        // Tile r + NS - 1 is asked for while tile r is computed; its pages were looked up a tile before
-        // (their wait is the scalar loads', apart from the copies').
-        uint32_t good[NS] = {};
-        Tile t = look(first);
-#pragma unroll
-        for (int i = 0; i < NS - 1; ++i)
-            if (i < tiles) {
-                issue(t, i);
-                good[i] = t.good;
-                t = look(first + (i + 1) * ROUND);
-            }
-        int stage = 0;
-        for (int r = 0; r < tiles; ++r) {
-            if (NS > 2 && r + 1 < tiles) wait_vmcnt<(NS - 2) * NL>();
-            else wait_vmcnt<0>();
-            if constexpr (WR > 1) barrier_lds();
-            const int next = stage >= 1 ? stage - 1 : NS - 1;
-            if (r + NS - 1 < tiles) {
-                issue(t, next);
-                good[NS - 1] = t.good;
-                t = look(first + (r + NS) * ROUND);
-            }
-            if (rows > 0) compute(ring + stage * S::TILE, good[0], first + r * ROUND);
-#pragma unroll
-            for (int i = 0; i + 1 < NS; ++i) good[i] = good[i + 1];
-            stage = stage + 1 < NS ? stage + 1 : 0;
+    auto compute = [&](int stage, uint32_t* good, int key0) {
+        if constexpr (ALIGNED && WR > 1) {
+            const u32x4_t is = *(const u32x4_t*)there_[stage];
+            good[0] &= __builtin_amdgcn_readfirstlane(is[0] | is[1]);
+            good[1] &= __builtin_amdgcn_readfirstlane(is[2] | is[3]);
         }
-    } else if (tiles > 0) {
-        Tile t = look(first);
-        issue(t, 0);
-        int stage = 0;
-        for (int r = 0; r < tiles; ++r) {
-            const uint32_t good = t.good;
-            settle(stage);
-            t = look(first + (r + 1) * ROUND);
-            if constexpr (WR > 1) barrier_lds();
-            else wave_lds_exchange();
-            if (r + 1 < tiles) issue(t, 0);
-            if (rows > 0) compute(ring + stage * S::TILE, good, first + r * ROUND);
-            wave_lds_exchange();
-            stage = stage + 1 < NS ? stage + 1 : 0;
+        bool plain = key0 >= rg.sure && key0 + KT <= rg.safe;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) plain = plain && good[n] == ~0u;
+        if (!plain) set_apart(stage, good, key0);
+        if (rows > 0) products(stage, plain, good, key0);
+    };
+    for (int r = 0; r < tiles; ++r) {
+        uint32_t good[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) good[n] = tile.good[n];
+        settle(r & 1);
+        if constexpr (ALIGNED) wait_vmcnt<0>();
+        if constexpr (WR > 1) barrier_lds();
+        else wave_lds_exchange();
+        if (r + 1 < tiles) {
+            issue(next, (r + 1) & 1);
+            tile = next;
+            next = look(first + (r + 2) * ROUND);
         }
+        compute(r & 1, good, first + r * ROUND);
+        wave_lds_exchange();
     }
 
     // ---- sums, and the groups' parts ----------------------------------------------------
@@ -531,7 +582,7 @@ __global__ __launch_bounds__((TreeShape<DP, E4M3, WR, RB>::WAVES * 64), (TreeSha
         sum[i] += __shfl_xor(sum[i], 32);
         // a NaN among the scores passed by the maximum: as an infinite one it makes
         // every later factor of this part NaN and of the others 0
-        if (sum[i] != sum[i]) mx[i] = -kNegInf;
+        mx[i] = sum[i] != sum[i] ? -kNegInf : mx[i] * scale;
     }
     // 4 elements from d on of a row with maximum m and sum l
     auto store = [&](int row, int d, f32x4_t a, float m, float l) {
@@ -668,6 +719,42 @@ __global__ __launch_bounds__(256) void tree_join_kernel(TreeArgs p) {
     }
 }
 
+// The same for few chunks: DL lanes a row, 256 / DL rows a workgroup, chunk by chunk.
+constexpr int kTreeFew = 16;
+template <class T, int DL>
+__global__ __launch_bounds__(256) void tree_join_few_kernel(TreeArgs p) {
+    const int row = blockIdx.x * (256 / DL) + threadIdx.x / DL, unit = blockIdx.y;
+    const int b = unit / p.Hk, hk = unit - b * p.Hk, d = threadIdx.x % DL * 4;
+    const int blk = min(row / p.rows, p.blocks - 1);
+    // (the block's number differs between the lanes, so its range is read by each)
+    const TreeRange rg = tree_range(p, b, blk);
+    if (row >= rg.m * p.G || d >= p.D) return;
+    const int n = tree_chunks(p, rg);
+    const int64_t at = ((int64_t)unit * p.blocks * p.rows + row) * p.splits;
+    float m[kTreeFew], l[kTreeFew], top = kNegInf, sum = 0.0f;
+    f32x4_t v[kTreeFew], a = {};
+#pragma unroll
+    for (int i = 0; i < kTreeFew; ++i) {
+        m[i] = i < n ? p.pml[2 * (at + i)] : kNegInf;
+        l[i] = i < n ? p.pml[2 * (at + i) + 1] : 0.0f;
+        v[i] = i < n ? *(const f32x4_t*)(p.po + (at + i) * p.D + d) : (f32x4_t){};
+        top = fmaxf(top, m[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kTreeFew; ++i) {
+        if (i >= n) continue;
+        const float f = m[i] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m[i] - top);
+        sum += m[i] == kNegInf ? 0.0f : f * l[i];
+        a += f * v[i];
+    }
+    const float z = top == kNegInf ? 0.0f : p.v_scale / sum;
+    const int t = row / p.G, h = hk * p.G + row - t * p.G;
+    T* out = (T*)p.out.p + (int64_t)(rg.row0 + t) * p.out.ts + (int64_t)h * p.out.hs + d;
+    store4<T>(out, a[0] * z, a[1] * z, a[2] * z, a[3] * z);
+    if (d == 0 && p.lse)
+        p.lse[(int64_t)(rg.row0 + t) * p.Hq + h] = top == kNegInf ? kNegInf : 0.6931471805599453f * top + logf(sum);
+}
+
 template <class T, int DP, bool E4M3, bool ALIGNED, int WR, int RB>
 hipError_t run_shape(const TreeArgs& a, hipStream_t st) {
     typedef TreeShape<DP, E4M3, WR, RB> S;
@@ -689,7 +776,9 @@ hipError_t run(const TreeArgs& a, hipStream_t st) {
     if (e != hipSuccess || a.splits == 1) return e;
     // a whole row a workgroup where that takes its chunks in kTreeJoinDeep turns, else 32 elements
     const dim3 rows(a.max_nodes * a.G, a.B * a.Hk);
-    if (a.splits <= kTreeJoinDeep * (256 / (DP / 4)))
+    if (a.splits <= kTreeFew)
+        hipLaunchKernelGGL((tree_join_few_kernel<T, DP / 4>), dim3((rows.x + 1024 / DP - 1) / (1024 / DP), rows.y), dim3(256), 0, st, a);
+    else if (a.splits <= kTreeJoinDeep * (256 / (DP / 4)))
         hipLaunchKernelGGL((tree_join_kernel<T, DP / 4>), rows, dim3(256), 0, st, a);
     else
         hipLaunchKernelGGL((tree_join_kernel<T, 8>), dim3(rows.x, rows.y, DP / 32), dim3(256), 0, st, a);

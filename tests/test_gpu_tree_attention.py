@@ -266,11 +266,13 @@ def test_views_and_in_place():
 
 
 def test_one_token_is_paged_attention():
-    """One new token per sequence: what paged_attention gives, within the rounding of the result."""
+    """One new token per sequence: what paged_attention gives, within the rounding of the results.  Either is off
+    by half a step and the sums' errors (2^-16 of the magnitudes, far below); so they may be a whole step apart,
+    and a bf16 step is 2^-7 of the value just above a power of two."""
     c = make(16, 4, 128, [1, 333, 2000, 64], [1] * 4, 16, BF, seed=6, tree=False, behind=0)
     out, lse = run(c)
     ref = tcm.paged_attention(c["q"], c["k"], c["v"], c["table"], c["lengths"])
-    assert ((out.float() - ref.float()).abs() <= 2.0 ** -8 * ref.float().abs() + 1e-6).all()
+    assert ((out.float() - ref.float()).abs() <= (2.0 ** -7 + 2.0 ** -12) * ref.float().abs() + 1e-6).all()
 
 
 def test_probabilities_far_below_the_largest():
