@@ -80,32 +80,15 @@ int64_t tree_blocks(int64_t G, int64_t D, int64_t max_nodes) {
     const int64_t n = cdiv(max_nodes * G, tree_rows(G, D, max_nodes));
     return n > 0 ? n : 1;
 }
-// The split over the length: into chunks for kTreeGroups workgroups, of 256 keys at least.
-constexpr int64_t kTreeGroups = 1024, kTreeMinChunk = 256;
-struct TreeSplit {
-    int64_t chunk, n;
-};
-TreeSplit tree_split(int64_t units, int64_t span) {
-    int64_t most = cdiv(kTreeGroups, units);
-    if (most > kTreeMaxSplits) most = kTreeMaxSplits;
-    TreeSplit s;
-    s.chunk = cdiv(cdiv(span, most), 128) * 128;
-    if (s.chunk < kTreeMinChunk) s.chunk = kTreeMinChunk;
-    s.n = cdiv(span, s.chunk);
-    if (s.n < 1) s.n = 1;
-    return s;
+// Workgroups of a call whose blocks of rows number at most `units`, of at most `span` keys each: one a tile of
+// the largest size, up to kTreeGroups.  A block of one tile is not split.
+int64_t tree_groups(int64_t units, int64_t span, int64_t round) {
+    const int64_t tiles = cdiv(span, round) > 0 ? cdiv(span, round) : 1;
+    return units > kTreeGroups / tiles ? kTreeGroups : units * tiles;
 }
-// No tree_split() of at most `units` and this span has more chunks over all of them (0: none has more
-// than one): u units have at most ceil(kTreeGroups / u) each, which is fewer than kTreeGroups + u
-// together, and one each from kTreeGroups units on.
-int64_t tree_most_chunks(int64_t units, int64_t span) {
-    int64_t n = cdiv(span, kTreeMinChunk);
-    if (n > kTreeMaxSplits) n = kTreeMaxSplits;
-    if (n <= 1) return 0;
-    const int64_t u = units < kTreeGroups ? units : kTreeGroups;
-    return u * n < kTreeGroups + u ? u * n : kTreeGroups + u;
+int64_t tree_workspace(int64_t groups, int64_t rows, int64_t D, int64_t span, int64_t round) {
+    return span > round ? groups * (2 * rows * (D + 2) * 4 + (int64_t)sizeof(TreeSplit)) : 0;
 }
-int64_t tree_workspace(int64_t chunks, int64_t rows, int64_t D) { return chunks * rows * (D + 2) * 4; }
 
 tcm_status check_tree_sizes(int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t max_nodes, int64_t max_len) {
     if (B < 0 || Hq < 0 || Hk < 0 || D < 1 || max_nodes < 0 || max_len < 0) return TCM_ERR_INVALID_SHAPE;
@@ -277,8 +260,9 @@ tcm_status tcm_paged_tree_attention_workspace(int64_t B, int64_t Hq, int64_t Hk,
     if (s != TCM_OK) return s;
     *bytes = 0;
     if (B == 0 || Hq == 0 || max_nodes == 0) return TCM_OK;
-    const int64_t G = Hq / Hk;
-    *bytes = tree_workspace(tree_most_chunks(B * Hk * tree_blocks(G, D, max_nodes), max_len), tree_rows(G, D, max_nodes), D);
+    // (tiles of E4M3 keys are at least as long; a window's first tile begins up to 31 keys early)
+    const int64_t G = Hq / Hk, rows = tree_rows(G, D, max_nodes), round = tree_round(rows, D, 2);
+    *bytes = tree_workspace(tree_groups(B * Hk * tree_blocks(G, D, max_nodes), max_len, round), rows, D, max_len, round);
     return TCM_OK;
 }
 
@@ -305,22 +289,19 @@ tcm_status tcm_paged_tree_attention(const tcm_heads* q, const tcm_cache* cache,
     // no page, no key
     if (cache->pages == 0) max_len = 0;
     const int64_t G = Hq / Hk, rows = tree_rows(G, D, max_nodes), blocks = tree_blocks(G, D, max_nodes);
-    // a block's tokens are up to max_nodes apart, and its first tile begins up to 31 keys before the first key
-    const int64_t span = window > 0 && window < max_len - max_nodes - 31 ? window + max_nodes + 31 : max_len;
-    const int64_t most = UINT32_MAX / 256;  // workgroups of a launch
-    if (B * Hk > most / blocks) return TCM_ERR_UNSUPPORTED_SHAPE;
-    const int64_t units = B * Hk * blocks;
-    const TreeSplit sp = tree_split(units, span);
-    if (sp.n > 1) {
+    if (B * Hk > kMaxRows / blocks) return TCM_ERR_UNSUPPORTED_SHAPE;
+    const bool e4m3 = cache->dtype == TCM_E4M3;
+    const int64_t round = tree_round(rows, D, e4m3 ? 1 : 2), groups = tree_groups(B * Hk * blocks, max_len, round);
+    const int64_t need = tree_workspace(groups, rows, D, max_len, round);
+    if (need > 0) {
         if (!workspace) return TCM_ERR_NULL_POINTER;
         if (!aligned16(workspace)) return TCM_ERR_MISALIGNED;
-        if (workspace_bytes < tree_workspace(units * sp.n, rows, D)) return TCM_ERR_WORKSPACE;
+        if (workspace_bytes < need) return TCM_ERR_WORKSPACE;
     }
     DeviceInfo dev;
     if ((s = device_info(&dev)) != TCM_OK) return s;
     TreeArgs a;
     memset(&a, 0, sizeof(a));
-    const bool e4m3 = cache->dtype == TCM_E4M3;
     const int64_t es = e4m3 ? 1 : 2;
     a.q = view(q, T, Hq);
     a.out = view(out, T, Hq);
@@ -339,9 +320,10 @@ tcm_status tcm_paged_tree_attention(const tcm_heads* q, const tcm_cache* cache,
     a.tree = (const uint32_t*)tree;
     a.tree_words = tree ? (int32_t)(2 * tree_words) : 0;
     a.lse = lse;
-    if (sp.n > 1) {
+    if (need > 0) {
         a.po = (float*)workspace;
-        a.pml = a.po + units * sp.n * rows * D;
+        a.pml = a.po + groups * 2 * rows * D;
+        a.split = (TreeSplit*)(a.pml + groups * 2 * rows * 2);
     }
     a.T = (int32_t)T;
     a.B = (int32_t)B;
@@ -361,9 +343,7 @@ tcm_status tcm_paged_tree_attention(const tcm_heads* q, const tcm_cache* cache,
     a.max_len = (int32_t)max_len;
     a.max_nodes = (int32_t)max_nodes;
     a.window = window > max_len ? 0 : (int32_t)window;
-    a.chunk = (int32_t)sp.chunk;
-    a.splits = (int32_t)sp.n;
-    a.blocks = (int32_t)blocks;
+    a.groups = (int32_t)groups;
     a.rows = (int32_t)rows;
     a.scale_log2 = scale * (e4m3 ? cache->k_scale : 1.0f) * 1.4426950408889634f;
     a.v_scale = e4m3 ? cache->v_scale : 1.0f;

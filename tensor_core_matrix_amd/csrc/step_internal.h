@@ -74,6 +74,11 @@ hipError_t launch_gemm_w4(const W4Args& a, int32_t dtype, bool e2m1, bool out_f3
 
 // ---- attention of drafted tokens (tree_attn.hip) ------------------------------------
 
+// A block of rows whose tiles lie in `parts` stretches, the first one that of the workgroup before (0: none).
+struct TreeSplit {
+    int32_t parts, b, hk, blk;
+};
+
 struct TreeArgs {
     HeadView q, out;
     const char* kc;
@@ -86,20 +91,26 @@ struct TreeArgs {
     const uint32_t* tree;  // NULL: a chain; else tree_words words a token
     int32_t tree_words;    // of 32 bits
     float* lse;
-    float* po;   // split: B x Hk x blocks x rows x splits x D partial sums,
-    float* pml;  // and as many pairs (maximum in base 2, sum)
+    float* po;   // 2 groups x rows x D partial sums of the blocks that lie in more than one stretch (NULL: none can),
+    float* pml;  // and as many pairs (maximum in base 2, sum),
+    TreeSplit* split;  // and what each stretch goes on with
     int32_t T, B, Hq, Hk, G, D;
     int32_t pages, page_size;
     uint32_t page_magic;  // n / page_size = n * page_magic >> page_shift for n < 2^31
     int32_t page_shift;
     int32_t max_len, max_nodes, window;
-    int32_t chunk, splits;
-    int32_t blocks;  // blocks of rows of one sequence and key-value head
-    int32_t rows;    // of a block: 16, 64 or 128
+    int32_t groups;  // workgroups, which share the tiles evenly
+    int32_t rows;    // of a block of one sequence's rows of a key-value head: 16, 64 or 128
     float scale_log2, v_scale;
 };
 
-constexpr int kTreeMaxSplits = 256;
+constexpr int kTreeGroups = 512;   // workgroups at most: two for each of 256 compute units
+constexpr int kTreeSetup = 3;      // what a block of rows takes beside its tiles, in tiles
+constexpr int kTreeLeast = 2;      // steps of a workgroup at least
+// Keys of a tile, the unit that is shared out (of all waves' tiles of 32 where waves have their own)
+constexpr int tree_round(int64_t rows, int64_t D, int64_t es) {
+    return rows > 16 ? 64 : 32 * ((D <= 64 ? 64 : D <= 128 ? 128 : 256) * es <= 256 ? 4 : 2);
+}
 
 hipError_t launch_tree_attention_bf16(const TreeArgs& a, bool e4m3, hipStream_t st);
 hipError_t launch_tree_attention_f16(const TreeArgs& a, bool e4m3, hipStream_t st);

@@ -19,8 +19,13 @@
 //
 // WR waves share the stages and take 16 RB rows each; WK groups of WR waves take every WK-th tile
 // and meet in LDS at the end.  16 rows or fewer: 1 x 4 and tiles of 32 keys, each wave stages of its own and no
-// barrier; more: 4 x 1 and tiles of 64, one barrier a tile.  With more than one chunk of keys tree_join_kernel joins
-// the parts.
+// barrier; more: 4 x 1 and tiles of 64, one barrier a tile.
+//
+// The work is dealt evenly: the tiles of all blocks of rows of all heads and sequences are numbered, and every
+// workgroup takes a stretch of as many, over the ends of blocks where they come.  (With a chunk of keys a
+// workgroup, sequences of different lengths left the device idle for half of the time.)  A block that lies in
+// one stretch is written at once; a stretch begins and ends inside a block at most once each, and tree_join_kernel
+// joins those parts.  The host sees no length, so each workgroup adds up the tiles of the sequences itself.
 //
 // Which keys a row sees is a word of 32 bits a tile, made for tiles that need it: those that reach
 // the sequence's own tokens, the window's edge, the end or a hole.  There a value that is not finite
@@ -45,37 +50,139 @@ struct TreeRange {
     int all;         // the sequence's tokens
     int context;     // keys before them
     int lo, end;     // the keys [lo, end) that any of the block's rows may see
-    int base;        // where the first tile begins
+    int base;        // where the first tile of the sequence begins
     int sure, safe;  // keys [sure, safe) are seen by every row
 };
-__device__ __forceinline__ TreeRange tree_range(const TreeArgs& p, int b, int blk) {
+// (starts and lengths of b as they were loaded)
+__device__ __forceinline__ TreeRange tree_sequence(const TreeArgs& p, int start, int stop, int length) {
     TreeRange r;
     const int64_t room = p.table_stride * (int64_t)p.page_size;
-    int len = min(max(scalar_int(p.lengths + b), 0), p.max_len);
+    int len = min(max(length, 0), p.max_len);
     if (len > room) len = (int)room;
-    r.row0 = max(scalar_int(p.starts + b), 0);
-    r.all = max(scalar_int(p.starts + b + 1) - r.row0, 0);
+    r.row0 = max(start, 0);
+    r.all = max(stop - r.row0, 0);
     r.m = max(min(min(r.all, p.max_nodes), p.T - r.row0), 0);
     r.context = max(len - r.all, 0);
-    const int first = blk * p.rows / p.G, last = min((blk * p.rows + p.rows - 1) / p.G, r.m - 1);
-    const bool chain = !p.tree;
-    r.end = chain ? min(len, r.context + last + 1) : len;
-    r.safe = chain ? min(len, r.context + first + 1) : r.context;
-    r.lo = r.sure = 0;
-    if (p.window > 0) {
-        // (a token's bits number 0 to `all`)
-        r.lo = max(0, chain ? r.context + first - p.window + 1 : r.context - p.window);
-        r.sure = max(0, chain ? r.context + last - p.window + 1 : min(r.context, r.context + r.all - p.window));
-    }
+    r.lo = p.window > 0 ? max(0, r.context - p.window + (p.tree ? 0 : 1)) : 0;
+    r.end = len;
     r.base = r.lo & ~31;
     return r;
 }
-// Chunks of it, at most p.splits (the last one takes what is left)
-__device__ __forceinline__ int tree_chunks(const TreeArgs& p, const TreeRange& r) {
-    return min((int)(((int64_t)max(r.end - r.base, 0) + p.chunk - 1) / p.chunk), p.splits);
+__device__ __forceinline__ TreeRange tree_range(const TreeArgs& p, int b, int blk) {
+    TreeRange r = tree_sequence(p, scalar_int(p.starts + b), scalar_int(p.starts + b + 1), scalar_int(p.lengths + b));
+    const int first = blk * p.rows / p.G, last = min((blk * p.rows + p.rows - 1) / p.G, r.m - 1);
+    const bool chain = !p.tree;
+    r.safe = chain ? min(r.end, r.context + first + 1) : r.context;
+    r.sure = 0;
+    if (p.window > 0) {
+        // (a token's bits number 0 to `all`)
+        if (chain) r.lo = max(0, r.context + first - p.window + 1);
+        r.sure = max(0, chain ? r.context + last - p.window + 1 : min(r.context, r.context + r.all - p.window));
+    }
+    if (chain) r.end = min(r.end, r.context + last + 1);
+    return r;
+}
+
+// The work in steps: a tile is one, and what a block of rows takes beside its tiles -- finding its keys, its
+// first copies and masks, and storing -- kTreeSetup, its first ones.  Stretches of them: `groups`, the first
+// `more` one longer than `each`.
+struct TreeShare {
+    int64_t each;
+    int groups, more;
+    __device__ __forceinline__ int64_t begin(int w) const { return w * each + min(w, more); }
+    __device__ __forceinline__ int owner(int64_t step) const {
+        const int64_t longer = more * (each + 1);
+        return step < longer ? (int)(step / (each + 1)) : more + (int)((step - longer) / each);
+    }
+};
+// A sequence that has steps: [before, before + cost), `tiles` + kTreeSetup for each block of rows of each head.
+struct TreePlace {
+    int64_t before, cost;
+    int b, blocks, tiles;
+};
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+    return (int64_t)(uint32_t)uniform((int)x) | (int64_t)uniform((int)(x >> 32)) << 32;
+}
+__device__ __forceinline__ int64_t lanes_before(int64_t x) {  // the sum of x over this lane and those before
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int64_t y = __shfl_up(x, d);
+        x += (int)(threadIdx.x & 63) >= d ? y : 0;
+    }
+    return x;
+}
+// The steps of 64 sequences, a lane each, `seen` before them (every lane of the wave is active)
+struct TreeLanes {
+    int64_t cost, sum;  // sum: with this sequence's
+    int blocks, tiles;
+};
+__device__ __forceinline__ TreeLanes tree_lanes(const TreeArgs& p, int b0, int round, int64_t seen) {
+    TreeLanes c = {0, 0, 0, 1};
+    const int b = b0 + (threadIdx.x & 63);
+    if (b < p.B) {
+        const TreeRange r = tree_sequence(p, p.starts[b], p.starts[b + 1], p.lengths[b]);
+        c.blocks = (r.m * p.G + p.rows - 1) / p.rows;
+        c.tiles = max((r.end - r.base + round - 1) / round, 1);
+        c.cost = (int64_t)c.blocks * (c.tiles + kTreeSetup) * p.Hk;
+    }
+    c.sum = seen + lanes_before(c.cost);
+    return c;
+}
+__device__ __forceinline__ TreeShare tree_share(const TreeArgs& p, int round, TreeLanes& lanes) {
+    lanes = tree_lanes(p, 0, round, 0);
+    int64_t total = uniform(__shfl(lanes.sum, 63));
+    for (int b0 = 64; b0 < p.B; b0 += 64) total = uniform(__shfl(tree_lanes(p, b0, round, total).sum, 63));
+    TreeShare s;
+    s.groups = (int)min(max(total / kTreeLeast, (int64_t)1), (int64_t)p.groups);
+    if (s.groups > 8) s.groups &= ~7;
+    s.each = total / s.groups;
+    s.more = (int)(total - s.each * s.groups);
+    return s;
+}
+// The sequence of a step; lanes: of the first 64
+__device__ __forceinline__ TreePlace tree_place(const TreeArgs& p, int round, int64_t step, const TreeLanes& lanes) {
+    TreeLanes c = lanes;
+    for (int b0 = 0;; b0 += 64) {
+        const uint64_t past = __ballot(step < c.sum);
+        if (past != 0 || b0 + 64 >= p.B) {
+            const int at = past != 0 ? __builtin_ctzll(past) : 63;
+            TreePlace r;
+            r.b = b0 + at;
+            r.cost = uniform(__shfl(c.cost, at));
+            r.before = uniform(__shfl(c.sum, at)) - r.cost;
+            r.blocks = uniform(__shfl(c.blocks, at));
+            r.tiles = uniform(__shfl(c.tiles, at));
+            return r;
+        }
+        c = tree_lanes(p, b0 + 64, round, uniform(__shfl(c.sum, 63)));
+    }
+}
+// The block of rows of a step: those of a head follow each other.
+struct TreeUnit {
+    int hk, blk;
+    int64_t first;  // its first step
+};
+__device__ __forceinline__ TreeUnit tree_unit(const TreePlace& s, int64_t step) {
+    const int64_t x = step - s.before, unit = x / (s.tiles + kTreeSetup);
+    TreeUnit u;
+    u.first = s.before + unit * (s.tiles + kTreeSetup);
+    u.hk = (int)(unit / s.blocks);
+    u.blk = (int)(unit - (int64_t)u.hk * s.blocks);
+    return u;
 }
 
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+
+// copy16_to_lds_asm() of a resource that may come out of vector registers (the compiler keeps scalars there that
+// have no place, and brings them back right before their use): five wait states between the vector
+// instruction that writes a scalar register and a memory instruction that reads it, which the compiler
+// does not insert before inline assembly.  It clobbers no memory: a copy fills the stage that nobody reads until
+// the next barrier, which does, and other accesses may be moved over it.
+__device__ __forceinline__ void copy16_to_lds_far(__amdgpu_buffer_rsrc_t r, void* lds_wave_base, uint32_t voffset) {
+    const uint32_t m0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds_wave_base;
+    asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" : : "v"(voffset), "s"(r), "{m0}"(m0));
+}
 
 // bits x .. 31 of a word, for any x
 __device__ __forceinline__ uint32_t bits_from(int x) { return x <= 0 ? ~0u : x >= 32 ? 0u : ~0u << x; }
@@ -111,7 +218,7 @@ struct TreeShape {
 // DP: D rounded up to 64, 128 or 256.  ALIGNED: page_size is a multiple of 16, so 16 keys from a multiple
 // of 16 on lie in one page.
 template <class T, int DP, bool E4M3, bool ALIGNED, int WR, int RB>
-__global__ __launch_bounds__((TreeShape<DP, E4M3, WR, RB>::WAVES * 64), (TreeShape<DP, E4M3, WR, RB>::LDS > 72 * 1024 ? 1 : 2)) void tree_kernel(TreeArgs p) {
+__global__ __launch_bounds__((TreeShape<DP, E4M3, WR, RB>::WAVES * 64), (DP > 128 || TreeShape<DP, E4M3, WR, RB>::LDS > 72 * 1024 ? 1 : 2)) void tree_kernel(TreeArgs p) {
     typedef TreeShape<DP, E4M3, WR, RB> S;
     typedef Half16<T> H;
     typedef typename H::x8 x8;
@@ -126,33 +233,62 @@ __global__ __launch_bounds__((TreeShape<DP, E4M3, WR, RB>::WAVES * 64), (TreeSha
     static_assert(NH * WR == 2 * NT, "a wave's copies");
     __shared__ __attribute__((aligned(1024))) char lds[S::LDS];
     __shared__ float lm_[RB][WK][16], ll_[RB][WK][16];
+    // ALIGNED, shared stages: whether the page of 16 keys of a stage is one
+    __shared__ __attribute__((aligned(16))) uint32_t there_[2][4];
+    // shared stages: whether a wave's part of the values holds one that is not finite
+    __shared__ __attribute__((aligned(16))) uint32_t strange_[2][4];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wr = wave % WR, wk = wave / WR;
     const int r16 = lane & 15, g4 = lane >> 4;
-    // Blocks of rows of one sequence and head read the same keys: their numbers are a multiple of 8
-    // apart where the heads' and sequences' count allows it, which is the same XCD.  The next chunk is
-    // moved on by one, so that the last chunks of all do not meet on one XCD.
-    const int units = p.B * p.Hk, per = units * p.blocks;
-    const int split = blockIdx.x / per, rest = blockIdx.x - split * per;
-    const int blk = rest / units, unit = (rest - blk * units + split) % units;
-    const int b = unit / p.Hk, hk = unit - b * p.Hk;
+    constexpr int ROUND = KT * WK;
+    TreeLanes lanes;
+    const TreeShare share = tree_share(p, ROUND, lanes);
+    if ((int)blockIdx.x >= share.groups) {
+        if (p.split && threadIdx.x == 0) p.split[blockIdx.x].parts = 0;
+        return;
+    }
+    // (stretches that follow each other, and so read the same keys now and then, on one XCD)
+    const int w = share.groups % 8 == 0 ? blockIdx.x % 8 * (share.groups / 8) + blockIdx.x / 8 : blockIdx.x;
+    int64_t step = share.begin(w);
+    const int64_t stop = share.begin(w + 1);
+    if (step >= stop) {  // (nothing to do at all)
+        if (p.split && threadIdx.x == 0) p.split[w].parts = 0;
+        return;
+    }
+    TreePlace place = tree_place(p, ROUND, step, lanes);
+    for (bool head = true;; head = false) {
+    const TreeUnit unit = tree_unit(place, step);
+    const int b = place.b, hk = unit.hk, blk = unit.blk;
+    // the tiles [tile0, tile1) of the block, of place.tiles
+    const int64_t tile_step = unit.first + kTreeSetup, past = unit.first + kTreeSetup + place.tiles;
+    const int tile0 = (int)max(step - tile_step, (int64_t)0), tile1 = (int)(min(stop, past) - tile_step);
+    if (head && p.split && threadIdx.x == 0) {
+        // A block whose first tiles are the stretch's before this one: its parts are this one's to announce.
+        TreeSplit s = {0, b, hk, blk};
+        if (step > tile_step && share.owner(tile_step) == w - 1) s.parts = share.owner(past - 1) - w + 2;
+        p.split[w] = s;
+    }
+    if (tile1 > 0) {
+    const bool part = tile1 - tile0 < place.tiles;
+    // this stretch's first or last part of a block
+    const int64_t slot = 2 * (int64_t)w + (tile0 == 0);
     const TreeRange rg = tree_range(p, b, blk);
-    if (blk * S::ROWS >= rg.m * p.G) return;
-    const int start = rg.base + split * p.chunk;
-    const int end = split + 1 == p.splits ? rg.end : (int)min((int64_t)rg.end, (int64_t)start + p.chunk);
-    if (p.splits > 1 && start >= end) return;
+    // the keys [start, end) of it
+    const int64_t from = rg.base + (int64_t)tile0 * ROUND;
+    const int start = (int)max(from, (int64_t)(rg.base + (rg.lo - rg.base) / ROUND * ROUND));
+    const int end = (int)min((int64_t)rg.end, rg.base + (int64_t)tile1 * ROUND);
 
     // this lane's rows (those past the last are the last, with zeros for q, and not stored)
     const int row0 = blk * S::ROWS + wr * 16 * RB;
     const int rows = rg.m * p.G - row0;  // of this wave and the later ones
-    int tok[RB], head[RB];
+    int tok[RB], qhead[RB];
 #pragma unroll
     for (int i = 0; i < RB; ++i) {
         const int row = row0 + min(16 * i + r16, rows - 1);
         tok[i] = row / p.G;
-        head[i] = hk * p.G + row - tok[i] * p.G;
+        qhead[i] = hk * p.G + row - tok[i] * p.G;
     }
 
     // ---- keys and values into LDS ---------------------------------------------------
@@ -166,8 +302,6 @@ __global__ __launch_bounds__((TreeShape<DP, E4M3, WR, RB>::WAVES * 64), (TreeSha
     const char* const kh = p.kc + hk * p.k_head;
     const char* const vh = p.vc + hk * p.v_head;
     auto page_of = [&](int key) { return (int)((uint64_t)(uint32_t)key * p.page_magic >> p.page_shift); };
-    // ALIGNED, shared stages: whether the page of 16 keys of a stage is one
-    __shared__ uint32_t there_[2][4];
     struct Tile {
         int key0;
         int page[NH];       // ALIGNED: of the 16 keys that the wave copies; else [0] of key l % KT of lane l
@@ -201,8 +335,19 @@ __global__ __launch_bounds__((TreeShape<DP, E4M3, WR, RB>::WAVES * 64), (TreeSha
         voff[q] = in ? key * (uint32_t)p.v_tok + piece * 16 : kOutOfRange;
     }
     u32x4_t held[ALIGNED ? 1 : 2 * NH * HALF];
-    auto issue = [&](Tile& t, int stage) {
-        char* const to = stages + stage * S::STAGE;
+    // A wave's copies of a tile, 2 NH HALF of them.  The memory pipe takes one in 16 cycles and more, and a wave that
+    // asks for the next one waits; so those of a whole tile are spread over the products before.
+    struct Copies {
+        __amdgpu_buffer_rsrc_t rk[NH], rv[NH];
+        char* to[NH];
+    };
+    auto copy = [&](const Copies& c, int i) {
+        const int y = i / (2 * HALF), q = i % HALF;
+        if (i / HALF % 2 == 0) copy16_to_lds_far(c.rk[y], c.to[y] + q * 1024, koff[q]);
+        else copy16_to_lds_far(c.rv[y], c.to[y] + KT * KB + q * 1024, voff[q]);
+    };
+    // Asks for a tile; false if its copies are left to the caller.
+    auto issue = [&](Tile& t, int stage, bool leave, Copies& c) {
         if constexpr (ALIGNED) {
             const bool whole = t.key0 >= rg.lo && t.key0 + KT <= end;
 #pragma unroll
@@ -210,31 +355,30 @@ __global__ __launch_bounds__((TreeShape<DP, E4M3, WR, RB>::WAVES * 64), (TreeSha
 #pragma unroll
             for (int y = 0; y < NH; ++y) {
                 const int h = WR > 1 ? wr : y;
-                const int key = t.key0 + 16 * h;
                 const uint32_t found = __builtin_amdgcn_readfirstlane(t.page[y]);
                 const bool is = found < (uint32_t)p.pages;
                 if constexpr (WR > 1) there_[stage][wr] = is ? 0xffffu << (wr & 1) * 16 : 0u;
                 else if (!is) t.good[0] &= h ? 0x0000ffffu : 0xffff0000u;
                 const uint32_t size = is ? kOutOfRange : 0u, page = is ? found : 0;
-                const uint32_t at = key - t.entry[y] * p.page_size;
-                const __amdgpu_buffer_rsrc_t rk = make_rsrc(kh + (page * (uint64_t)p.k_page + at * (uint64_t)p.k_tok), size);
-                const __amdgpu_buffer_rsrc_t rv = make_rsrc(vh + (page * (uint64_t)p.v_page + at * (uint64_t)p.v_tok), size);
-                char* const dk = to + h * 16 * KB;
-                char* const dv = dk + KT * KB;
-                if (whole) {
+                const uint32_t at = t.key0 + 16 * h - t.entry[y] * p.page_size;
+                c.rk[y] = make_rsrc(kh + (page * (uint64_t)p.k_page + at * (uint64_t)p.k_tok), size);
+                c.rv[y] = make_rsrc(vh + (page * (uint64_t)p.v_page + at * (uint64_t)p.v_tok), size);
+                c.to[y] = stages + stage * S::STAGE + h * 16 * KB;
+            }
+            if (whole) {
+                if (leave) return false;
 #pragma unroll
-                    for (int q = 0; q < HALF; ++q) copy16_to_lds_asm(rk, dk + q * 1024, koff[q]);
+                for (int i = 0; i < 2 * NH * HALF; ++i) copy(c, i);
+            } else {
 #pragma unroll
-                    for (int q = 0; q < HALF; ++q) copy16_to_lds_asm(rv, dv + q * 1024, voff[q]);
-                } else {
+                for (int y = 0; y < NH; ++y)
 #pragma unroll
                     for (int q = 0; q < HALF; ++q) {
-                        const int k = key + q * KN + kr;
+                        const int k = t.key0 + 16 * (WR > 1 ? wr : y) + q * KN + kr;
                         const bool in = k >= rg.lo && k < end;
-                        copy16_to_lds_asm(rk, dk + q * 1024, in ? koff[q] : kOutOfRange);
-                        copy16_to_lds_asm(rv, dv + q * 1024, in ? voff[q] : kOutOfRange);
+                        copy16_to_lds_far(c.rk[y], c.to[y] + q * 1024, in ? koff[q] : kOutOfRange);
+                        copy16_to_lds_far(c.rv[y], c.to[y] + KT * KB + q * 1024, in ? voff[q] : kOutOfRange);
                     }
-                }
             }
         } else {
             const bool ok = (uint32_t)t.page[0] < (uint32_t)p.pages;
@@ -257,6 +401,7 @@ __global__ __launch_bounds__((TreeShape<DP, E4M3, WR, RB>::WAVES * 64), (TreeSha
                     }
                 }
         }
+        return true;
     };
     // what issue() left in registers
     auto settle = [&](int stage) {
@@ -276,11 +421,9 @@ __global__ __launch_bounds__((TreeShape<DP, E4M3, WR, RB>::WAVES * 64), (TreeSha
     // Tile r + 1 is asked for while tile r is computed; its pages were looked up a tile before, by loads that
     // the wait for tile r's copies covers.  (A scalar load's wait would be the next one for an operand from
     // LDS, since both have one counter.)
-    constexpr int ROUND = KT * WK;
     const int first = start + KT * wk;
     const int tiles = first < end ? (end - first + ROUND - 1) / ROUND : 0;
     Tile tile = look(first);
-    if (tiles > 0) issue(tile, 0);
     Tile next = look(first + ROUND);
 
     // Q as the second operand: lane l holds row l % 16 and 8 elements of each step.  Elements of step
@@ -291,13 +434,15 @@ __global__ __launch_bounds__((TreeShape<DP, E4M3, WR, RB>::WAVES * 64), (TreeSha
     x8 qf[RB][STEPS];
 #pragma unroll
     for (int i = 0; i < RB; ++i) {
-        const T* row = (const T*)p.q.p + (int64_t)(rg.row0 + tok[i]) * p.q.ts + (int64_t)head[i] * p.q.hs;
+        const T* row = (const T*)p.q.p + (int64_t)(rg.row0 + tok[i]) * p.q.ts + (int64_t)qhead[i] * p.q.hs;
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) {
             const int e = E4M3 ? 64 * (s >> 1) + 16 * g4 + 8 * (s & 1) : 32 * s + 8 * g4;
             qf[i][s] = 16 * i + r16 < rows && e < p.D ? *(const x8*)(row + e) : (x8){};
         }
     }
+    Copies copies;
+    if (tiles > 0) issue(tile, 0, false, copies);
     // The first key of the context that a row sees (a chain: of all keys)
     int low[RB];
 #pragma unroll
@@ -357,12 +502,18 @@ __global__ __launch_bounds__((TreeShape<DP, E4M3, WR, RB>::WAVES * 64), (TreeSha
         int own_lane = lane;
         asm volatile("" : "+v"(own_lane));
         bool strange = false;
-        for (int i = own_lane * 16; i < KT * KB; i += 1024) {
+        for (int i = (wr * 64 + own_lane) * 16; i < KT * KB; i += WR * 1024) {
             const u32x4_t v = *(const u32x4_t*)(vt + i);
 #pragma unroll
             for (int y = 0; y < 4; ++y) strange = strange || not_finite<T, E4M3>(v[y]);
         }
-        if (!__any(strange)) return;  // (the waves that share the stage agree: they look at the same values)
+        if constexpr (WR > 1) {  // (a part of the stage a wave, and all of them come by here)
+            strange_[stage][wr] = __any(strange);
+            barrier_lds();
+            const u32x4_t any = *(const u32x4_t*)strange_[stage];
+            strange = any[0] | any[1] | any[2] | any[3];
+        }
+        if (!__any(strange)) return;
         if (rows > 0)
 #pragma unroll
             for (int i = 0; i < RB; ++i)
@@ -408,39 +559,57 @@ __global__ __launch_bounds__((TreeShape<DP, E4M3, WR, RB>::WAVES * 64), (TreeSha
         if constexpr (WR > 1) barrier_lds();
         else wave_lds_exchange();
     };
-    auto products = [&](int stage, bool plain, const uint32_t* good, int key0) {
-        const char* const kt = stages + stage * S::STAGE;
-        const char* const vt = kt + KT * KB;
-        float x[RB][8 * NT];
-        f32x4_t s[RB][2 * NT];
+    // The scores of a tile; SPREAD: with the copies of the next one among the products.
+    auto scores = [&](auto spread, const char* kt, f32x4_t (*s)[2 * NT]) {
+        constexpr int QS = E4M3 ? STEPS / 2 : STEPS, GROUPS = QS * 2 * NT, COPIES = 2 * NH * HALF;
 #pragma unroll
         for (int i = 0; i < RB; ++i)
 #pragma unroll
             for (int h = 0; h < 2 * NT; ++h) s[i][h] = (f32x4_t){};
+        i32x4_t kf[2][2 * NT];
+        auto read = [&](int st) {
 #pragma unroll
-        for (int st = 0; st < STEPS; st += E4M3 ? 2 : 1)
+            for (int h = 0; h < 2 * NT; ++h)
+                kf[st & 1][h] = *(const i32x4_t*)(kt + (16 * h + r16) * KB + ((4 * st + g4) ^ swz(r16)) * 16);
+        };
+        read(0);
+#pragma unroll
+        for (int st = 0; st < QS; ++st) {
+            if (st + 1 < QS) read(st + 1);
 #pragma unroll
             for (int h = 0; h < 2 * NT; ++h) {
-                const char* row = kt + (16 * h + r16) * KB;
-                const int sw = swz(r16);
+                const i32x4_t w = kf[st & 1][h];
                 if constexpr (E4M3) {
-                    const i32x4_t w4 = *(const i32x4_t*)(row + ((2 * st + g4) ^ sw) * 16);
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
                         u32x4_t u;
-                        u[0] = H::from_fp8(w4[2 * y], false);
-                        u[1] = H::from_fp8(w4[2 * y], true);
-                        u[2] = H::from_fp8(w4[2 * y + 1], false);
-                        u[3] = H::from_fp8(w4[2 * y + 1], true);
+                        u[0] = H::from_fp8(w[2 * y], false);
+                        u[1] = H::from_fp8(w[2 * y], true);
+                        u[2] = H::from_fp8(w[2 * y + 1], false);
+                        u[3] = H::from_fp8(w[2 * y + 1], true);
 #pragma unroll
-                        for (int i = 0; i < RB; ++i) s[i][h] = H::mma(__builtin_bit_cast(x8, u), qf[i][st + y], s[i][h]);
+                        for (int i = 0; i < RB; ++i) s[i][h] = H::mma(__builtin_bit_cast(x8, u), qf[i][2 * st + y], s[i][h]);
                     }
                 } else {
-                    const x8 kf = *(const x8*)(row + ((4 * st + g4) ^ sw) * 16);
 #pragma unroll
-                    for (int i = 0; i < RB; ++i) s[i][h] = H::mma(kf, qf[i][st], s[i][h]);
+                    for (int i = 0; i < RB; ++i) s[i][h] = H::mma(__builtin_bit_cast(x8, w), qf[i][st], s[i][h]);
+                }
+                if constexpr (decltype(spread)::value) {
+                    const int g = st * 2 * NT + h;
+#pragma unroll
+                    for (int i = 0; i < COPIES; ++i)
+                        if (i * GROUPS / COPIES == g) copy(copies, i);
                 }
             }
+        }
+    };
+    auto products = [&](int stage, bool plain, bool spread, const uint32_t* good, int key0) {
+        const char* const kt = stages + stage * S::STAGE;
+        const char* const vt = kt + KT * KB;
+        float x[RB][8 * NT];
+        f32x4_t s[RB][2 * NT];
+        if (spread) scores(std::true_type{}, kt, s);
+        else scores(std::false_type{}, kt, s);
 #pragma unroll
         for (int i = 0; i < RB; ++i)
 #pragma unroll
@@ -483,6 +652,7 @@ __global__ __launch_bounds__((TreeShape<DP, E4M3, WR, RB>::WAVES * 64), (TreeSha
                 }
             }
         };
+        read_values(0, 0);
         float top[RB];
         bool higher = false;
 #pragma unroll
@@ -509,7 +679,7 @@ __global__ __launch_bounds__((TreeShape<DP, E4M3, WR, RB>::WAVES * 64), (TreeSha
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            read_values(n, 0);
+            if (n > 0) read_values(n, 0);
             x8 upper[RB], lower[RB];
 #pragma unroll
             for (int i = 0; i < RB; ++i) {
@@ -546,7 +716,7 @@ __global__ __launch_bounds__((TreeShape<DP, E4M3, WR, RB>::WAVES * 64), (TreeSha
         }
     };
 
-    auto compute = [&](int stage, uint32_t* good, int key0) {
+    auto compute = [&](int stage, uint32_t* good, int key0, bool spread) {
         if constexpr (ALIGNED && WR > 1) {
             const u32x4_t is = *(const u32x4_t*)there_[stage];
             good[0] &= __builtin_amdgcn_readfirstlane(is[0] | is[1]);
@@ -556,7 +726,7 @@ __global__ __launch_bounds__((TreeShape<DP, E4M3, WR, RB>::WAVES * 64), (TreeSha
 #pragma unroll
         for (int n = 0; n < NT; ++n) plain = plain && good[n] == ~0u;
         if (!plain) set_apart(stage, good, key0);
-        if (rows > 0) products(stage, plain, good, key0);
+        if (rows > 0) products(stage, plain, spread, good, key0);
     };
     for (int r = 0; r < tiles; ++r) {
         uint32_t good[NT];
@@ -566,12 +736,13 @@ __global__ __launch_bounds__((TreeShape<DP, E4M3, WR, RB>::WAVES * 64), (TreeSha
         if constexpr (ALIGNED) wait_vmcnt<0>();
         if constexpr (WR > 1) barrier_lds();
         else wave_lds_exchange();
+        bool spread = false;
         if (r + 1 < tiles) {
-            issue(next, (r + 1) & 1);
+            spread = !issue(next, (r + 1) & 1, rows > 0, copies);
             tile = next;
             next = look(first + (r + 2) * ROUND);
         }
-        compute(r & 1, good, first + r * ROUND);
+        compute(r & 1, good, first + r * ROUND, spread);
         wave_lds_exchange();
     }
 
@@ -586,8 +757,8 @@ __global__ __launch_bounds__((TreeShape<DP, E4M3, WR, RB>::WAVES * 64), (TreeSha
     }
     // 4 elements from d on of a row with maximum m and sum l
     auto store = [&](int row, int d, f32x4_t a, float m, float l) {
-        if (p.splits > 1) {
-            const int64_t at = (((int64_t)unit * p.blocks) * S::ROWS + row) * p.splits + split;
+        if (part) {
+            const int64_t at = slot * S::ROWS + row - blk * S::ROWS;
             *(f32x4_t*)(p.po + at * p.D + d) = a;
             if (d == 0) {
                 p.pml[2 * at] = m;
@@ -655,111 +826,106 @@ __global__ __launch_bounds__((TreeShape<DP, E4M3, WR, RB>::WAVES * 64), (TreeSha
             }
         }
     }
+
+    }
+    step = past;
+    if (step >= stop) return;
+    if (step >= place.before + place.cost) place = tree_place(p, ROUND, step, lanes);
+    __syncthreads();  // (the stages, and what met in LDS, are free)
+    }
 }
 
-// Joins the chunks of one row: DL lanes x 4 elements (blockIdx.z picks which), 256 / DL chunks
-// at a time, at most kJoinDeep times.  Every load of a part is under way before the weights
-// that it waits for are computed.
-constexpr int kTreeJoinDeep = 8;
+// Joins the parts of the blocks of rows that lie in more than one stretch, DL lanes a row; with many parts all lanes
+// take one row after the other.
 template <class T, int DL>
 __global__ __launch_bounds__(256) void tree_join_kernel(TreeArgs p) {
-    __shared__ float wt[kTreeMaxSplits];
+    constexpr int RG = 256 / DL, FEW = 16;
+    __shared__ float wt[kTreeGroups];
     __shared__ float red[2][4];
-    __shared__ __attribute__((aligned(16))) float join[256 / DL][DL * 4];
-    constexpr int PARTS = 256 / DL;
-    const int row = blockIdx.x, unit = blockIdx.y;  // of p.max_nodes * p.G rows of each sequence and head
-    const int b = unit / p.Hk, hk = unit - b * p.Hk;
-    const int blk = row / p.rows;
-    const TreeRange rg = tree_range(p, b, blk);
-    if (row >= rg.m * p.G) return;
-    const int n = tree_chunks(p, rg);
-    const int64_t at0 = ((int64_t)unit * p.blocks * p.rows + row) * p.splits;
-    const float* ml = p.pml + 2 * at0;
-    const int c = threadIdx.x;
-    const int dl = (c % DL) * 4, d = blockIdx.z * DL * 4 + dl, part = c / DL;
-    const float m = c < n ? ml[2 * c] : kNegInf;
-    const float lc = c < n ? ml[2 * c + 1] : 0.0f;
-    f32x4_t v[kTreeJoinDeep];
-#pragma unroll
-    for (int i = 0; i < kTreeJoinDeep; ++i) {
-        const int at = part + i * PARTS;
-        v[i] = at < n && d < p.D ? *(const f32x4_t*)(p.po + (at0 + at) * p.D + d) : (f32x4_t){};
-    }
-    float top = m;
-#pragma unroll
-    for (int x = 1; x < 64; x *= 2) top = fmaxf(top, __shfl_xor(top, x));
-    if ((c & 63) == 0) red[0][c >> 6] = top;
-    __syncthreads();
-    top = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
-    const float f = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - top);
-    wt[c] = f;
-    float l = m == kNegInf ? 0.0f : f * lc;
-#pragma unroll
-    for (int x = 1; x < 64; x *= 2) l += __shfl_xor(l, x);
-    if ((c & 63) == 0) red[1][c >> 6] = l;
-    __syncthreads();
-    l = red[1][0] + red[1][1] + red[1][2] + red[1][3];
-    f32x4_t a = {};
-#pragma unroll
-    for (int i = 0; i < kTreeJoinDeep; ++i) {
-        const int at = part + i * PARTS;
-        if (at < n) a += wt[at] * v[i];
-    }
-    *(f32x4_t*)&join[part][dl] = a;
-    __syncthreads();
-    if (part == 0 && d < p.D) {
-#pragma unroll
-        for (int i = 1; i < PARTS; ++i) a += *(f32x4_t*)&join[i][dl];
+    __shared__ __attribute__((aligned(16))) float join[RG][DL * 4];
+    const TreeSplit unit = p.split[blockIdx.x + 1];
+    const int n = unit.parts, w0 = blockIdx.x;
+    if (n == 0) return;
+    const TreeRange rg = tree_range(p, unit.b, unit.blk);
+    const int rows = min(rg.m * p.G - unit.blk * p.rows, p.rows);
+    const int c = threadIdx.x, d = c % DL * 4, g = c / DL;
+    // part i of row r: in place 2 (w0 + i) + 1 for the first, which ends its stretch, else 2 (w0 + i)
+    auto place_of = [&](int i, int r) { return (2 * (int64_t)(w0 + i) + (i == 0)) * p.rows + r; };
+    auto store = [&](int r, f32x4_t a, float top, float l) {
+        const int row = unit.blk * p.rows + r, t = row / p.G, h = unit.hk * p.G + row - t * p.G;
         const float z = top == kNegInf ? 0.0f : p.v_scale / l;
-        const int t = row / p.G, h = hk * p.G + row - t * p.G;
         T* out = (T*)p.out.p + (int64_t)(rg.row0 + t) * p.out.ts + (int64_t)h * p.out.hs + d;
         store4<T>(out, a[0] * z, a[1] * z, a[2] * z, a[3] * z);
         if (d == 0 && p.lse)
             p.lse[(int64_t)(rg.row0 + t) * p.Hq + h] = top == kNegInf ? kNegInf : 0.6931471805599453f * top + logf(l);
-    }
-}
-
-// The same for few chunks: DL lanes a row, 256 / DL rows a workgroup, chunk by chunk.
-constexpr int kTreeFew = 16;
-template <class T, int DL>
-__global__ __launch_bounds__(256) void tree_join_few_kernel(TreeArgs p) {
-    const int row = blockIdx.x * (256 / DL) + threadIdx.x / DL, unit = blockIdx.y;
-    const int b = unit / p.Hk, hk = unit - b * p.Hk, d = threadIdx.x % DL * 4;
-    const int blk = min(row / p.rows, p.blocks - 1);
-    // (the block's number differs between the lanes, so its range is read by each)
-    const TreeRange rg = tree_range(p, b, blk);
-    if (row >= rg.m * p.G || d >= p.D) return;
-    const int n = tree_chunks(p, rg);
-    const int64_t at = ((int64_t)unit * p.blocks * p.rows + row) * p.splits;
-    float m[kTreeFew], l[kTreeFew], top = kNegInf, sum = 0.0f;
-    f32x4_t v[kTreeFew], a = {};
+    };
+    if (n <= FEW) {
+        const int r = blockIdx.y * RG + g;
+        if (r >= rows || d >= p.D) return;
+        float m[FEW], l[FEW], top = kNegInf, sum = 0.0f;
+        f32x4_t v[FEW], a = {};
 #pragma unroll
-    for (int i = 0; i < kTreeFew; ++i) {
-        m[i] = i < n ? p.pml[2 * (at + i)] : kNegInf;
-        l[i] = i < n ? p.pml[2 * (at + i) + 1] : 0.0f;
-        v[i] = i < n ? *(const f32x4_t*)(p.po + (at + i) * p.D + d) : (f32x4_t){};
-        top = fmaxf(top, m[i]);
-    }
+        for (int i = 0; i < FEW; ++i) {
+            const int64_t at = place_of(min(i, n - 1), r);
+            m[i] = i < n ? p.pml[2 * at] : kNegInf;
+            l[i] = i < n ? p.pml[2 * at + 1] : 0.0f;
+            v[i] = i < n ? *(const f32x4_t*)(p.po + at * p.D + d) : (f32x4_t){};
+            top = fmaxf(top, m[i]);
+        }
 #pragma unroll
-    for (int i = 0; i < kTreeFew; ++i) {
-        if (i >= n) continue;
-        const float f = m[i] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m[i] - top);
-        sum += m[i] == kNegInf ? 0.0f : f * l[i];
-        a += f * v[i];
+        for (int i = 0; i < FEW; ++i) {
+            if (i >= n || m[i] == kNegInf) continue;
+            const float f = __builtin_amdgcn_exp2f(m[i] - top);
+            sum += f * l[i];
+            a += f * v[i];
+        }
+        store(r, a, top, sum);
+        return;
     }
-    const float z = top == kNegInf ? 0.0f : p.v_scale / sum;
-    const int t = row / p.G, h = hk * p.G + row - t * p.G;
-    T* out = (T*)p.out.p + (int64_t)(rg.row0 + t) * p.out.ts + (int64_t)h * p.out.hs + d;
-    store4<T>(out, a[0] * z, a[1] * z, a[2] * z, a[3] * z);
-    if (d == 0 && p.lse)
-        p.lse[(int64_t)(rg.row0 + t) * p.Hq + h] = top == kNegInf ? kNegInf : 0.6931471805599453f * top + logf(sum);
+    for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+        float top = kNegInf, l = 0.0f;
+        for (int i = c; i < n; i += 256) top = fmaxf(top, p.pml[2 * place_of(i, r)]);
+#pragma unroll
+        for (int x = 1; x < 64; x *= 2) top = fmaxf(top, __shfl_xor(top, x));
+        if ((c & 63) == 0) red[0][c >> 6] = top;
+        __syncthreads();
+        top = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+        for (int i = c; i < n; i += 256) {
+            const float m = p.pml[2 * place_of(i, r)];
+            const float f = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - top);
+            wt[i] = f;
+            l += m == kNegInf ? 0.0f : f * p.pml[2 * place_of(i, r) + 1];
+        }
+#pragma unroll
+        for (int x = 1; x < 64; x *= 2) l += __shfl_xor(l, x);
+        if ((c & 63) == 0) red[1][c >> 6] = l;
+        __syncthreads();
+        l = red[1][0] + red[1][1] + red[1][2] + red[1][3];
+        f32x4_t a = {};
+        if (d < p.D)
+#pragma unroll 4
+            for (int i = g; i < n; i += RG) a += wt[i] * *(const f32x4_t*)(p.po + place_of(i, r) * p.D + d);
+        *(f32x4_t*)&join[g][d] = a;
+        __syncthreads();
+        if (g == 0 && d < p.D) {
+#pragma unroll
+            for (int i = 1; i < RG; ++i) a += *(f32x4_t*)&join[i][d];
+            store(r, a, top, l);
+        }
+        __syncthreads();  // (the arrays are free)
+    }
 }
 
 template <class T, int DP, bool E4M3, bool ALIGNED, int WR, int RB>
 hipError_t run_shape(const TreeArgs& a, hipStream_t st) {
     typedef TreeShape<DP, E4M3, WR, RB> S;
-    const dim3 grid((uint32_t)a.splits * a.B * a.Hk * a.blocks);
-    hipLaunchKernelGGL((tree_kernel<T, DP, E4M3, ALIGNED, WR, RB>), grid, dim3(S::WAVES * 64), 0, st, a);
+    hipLaunchKernelGGL((tree_kernel<T, DP, E4M3, ALIGNED, WR, RB>), dim3(a.groups), dim3(S::WAVES * 64), 0, st, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !a.po) return e;
+    // (few parts: 256 / (DP / 4) rows a workgroup; many: rows y, y + the grid's, .. one by one)
+    constexpr int RG = 256 / (DP / 4);
+    const int rows = min(S::ROWS, a.max_nodes * a.G), least = (S::ROWS + RG - 1) / RG;
+    hipLaunchKernelGGL((tree_join_kernel<T, DP / 4>), dim3(a.groups - 1, min(rows, max(least, 32))), dim3(256), 0, st, a);
     return hipGetLastError();
 }
 template <class T, int DP, bool E4M3, bool ALIGNED>
@@ -772,17 +938,7 @@ hipError_t run_main(const TreeArgs& a, hipStream_t st) {
 
 template <class T, int DP, bool E4M3>
 hipError_t run(const TreeArgs& a, hipStream_t st) {
-    const hipError_t e = a.page_size % 16 == 0 ? run_main<T, DP, E4M3, true>(a, st) : run_main<T, DP, E4M3, false>(a, st);
-    if (e != hipSuccess || a.splits == 1) return e;
-    // a whole row a workgroup where that takes its chunks in kTreeJoinDeep turns, else 32 elements
-    const dim3 rows(a.max_nodes * a.G, a.B * a.Hk);
-    if (a.splits <= kTreeFew)
-        hipLaunchKernelGGL((tree_join_few_kernel<T, DP / 4>), dim3((rows.x + 1024 / DP - 1) / (1024 / DP), rows.y), dim3(256), 0, st, a);
-    else if (a.splits <= kTreeJoinDeep * (256 / (DP / 4)))
-        hipLaunchKernelGGL((tree_join_kernel<T, DP / 4>), rows, dim3(256), 0, st, a);
-    else
-        hipLaunchKernelGGL((tree_join_kernel<T, 8>), dim3(rows.x, rows.y, DP / 32), dim3(256), 0, st, a);
-    return hipGetLastError();
+    return a.page_size % 16 == 0 ? run_main<T, DP, E4M3, true>(a, st) : run_main<T, DP, E4M3, false>(a, st);
 }
 
 }  // namespace

@@ -137,8 +137,8 @@ def test_tree_refusals():
         assert tree(**kw) == MISALIGNED, kw
     for kw in (dict(dt=tcm.F32), dict(c=cache(dt=tcm.F16))):
         assert tree(**kw) == UNSUP_DTYPE, kw
-    assert tree(B=65535, Hq=4096, Hk=4096, q=heads(ts=4096 * 64), out=heads(P[7], ts=4096 * 64), most=100) == UNSUP_SHAPE
-    assert tree(nb=0) == WORKSPACE and tree(nb=0, ws=None, most=256) in PASSED
+    need = tcm.paged_tree_attention_workspace(2, 8, 2, 64, 8, 1024)
+    assert tree(nb=need - 1) == WORKSPACE and tree(nb=need) in PASSED and tree(nb=0, ws=None, most=64) in PASSED
 
 
 def test_tree_workspaces_cover_smaller_calls():
