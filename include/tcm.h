@@ -592,12 +592,14 @@ tcm_status tcm_add_rms_norm_bwd_workspace(int64_t T, int64_t D, int64_t* bytes);
  *            E8M0 bytes (255: NaN), as tcm_gemm_mx_fp4 takes them; group 32, zeros NULL
  *   Out      M x N of out_dtype (dtype or TCM_F32), rows ldo >= N elements apart
  * Elements enter the products as they are, and sums are fp32; scales multiply fp32 sums
- * of a group.  The result is rounded once.  With TCM_U4 the products with q and with zero are
- * summed apart and subtracted, so errors go by scale * (q + zero): the result r
- * satisfies |r - exact| <= u sum_k |x_k| scale (q + zero) (E2M1: |x_k w_k|), u = 2^-17 for K <= 16384
- * and 2^-12 beyond, plus the rounding; a row of X with a value that is not finite gives NaN there.  Rows of X do not
- * reach each other's results.  The weights are read once for each 64 rows.  K a multiple of 32, at most 2^20; ldx a multiple of 8 and at
- * most 2^21; X and W 16-byte aligned, scales and Out by their element.  Out overlaps no input.
+ * of a group.  The result is rounded once.  With TCM_U4 the products with q and with zero may be
+ * summed apart and subtracted (they are for TCM_BF16), so errors go by scale * (q + zero):
+ * the result r satisfies |r - exact| <= u sum_k |x_k| scale (q + zero) (E2M1: |x_k w_k|),
+ * u = 2^-17 for K <= 16384 and 2^-12 beyond, plus the rounding.  A row of X with a value that
+ * is not finite has no finite result; rows do not reach each other's results.  The weights
+ * are read once for each 64 rows, fastest where K is a multiple of 128 and scales and zeros
+ * are 8-byte aligned.  K a multiple of 32, at most 2^20; ldx a multiple of 8 and at most 2^21;
+ * X and W 16-byte aligned, scales and Out by their element.  Out overlaps no input.
  */
 tcm_status tcm_gemm_w4(const void* X, int64_t ldx, const void* W, const void* scales,
                        const void* zeros, void* Out, int64_t ldo, int64_t M, int64_t N, int64_t K,

@@ -68,6 +68,8 @@ struct W4Args {
     int32_t gchunks;  // chunks of 32 values of a group
     int32_t gshift;   // log2 of it where it is a power of two, else -1
     int32_t groups;   // groups of a row
+    // set by the launch: rows of a workgroup, its waves side by side, and the values of a row of X in LDS at once
+    int32_t rows, wn, kc;
 };
 
 hipError_t launch_gemm_w4(const W4Args& a, int32_t dtype, bool e2m1, bool out_f32, int cus, hipStream_t st);
