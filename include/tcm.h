@@ -595,7 +595,7 @@ tcm_status tcm_add_rms_norm_bwd_workspace(int64_t T, int64_t D, int64_t* bytes);
  * of a group.  The result is rounded once.  With TCM_U4 the products with q and with zero may be
  * summed apart and subtracted (they are for TCM_BF16), so errors go by scale * (q + zero):
  * the result r satisfies |r - exact| <= u sum_k |x_k| scale (q + zero) (E2M1: |x_k w_k|),
- * u = 2^-17 for K <= 16384 and 2^-12 beyond, plus the rounding.  A row of X with a value that
+ * u = (K / 32 + 96) 2^-24, plus the rounding.  A row of X with a value that
  * is not finite has no finite result; rows do not reach each other's results.  The weights
  * are read once for each 64 rows, fastest where K is a multiple of 128 and scales and zeros
  * are 8-byte aligned.  K a multiple of 32, at most 2^20; ldx a multiple of 8 and at most 2^21;

@@ -1,13 +1,12 @@
 // Out = X W^T for few rows X and 4-bit weights W.
 //
-// Bound by memory while X has few rows, since every 64 rows pass over the weights once; from about 40 rows on by the
-// instructions that unpack a word (about 90 vector instructions a block of 16 x 128, the same for any number
-// of rows, and 2 for each 16 rows and group).  Measured on an MI355X, weights as a rule not in a cache:
+// Bound by memory while X has few rows, since every 64 rows pass over the weights once; from about 40 rows on loads, unpacking (about 90
+// vector instructions a block of 16 x 128) and X's way through LDS take about the same time each.  Measured on an MI355X, weights as a rule not in a cache:
 //
 //   M   N      K     elements, group, type      us     weights and scales, TB/s
 //   1   4096   4096  U4, 128, zeros, bf16       8.3    1.1  (an empty call of this library takes 7)
 //   12  12288  4096  E2M1, 32, bf16             14.8   1.8
-//   48  32003  4096  U4, 64, fp16 to fp32       29.4   2.4
+//   48  32003  4096  U4, 64, fp16 to fp32       28.5   2.4
 //
 // A wave takes 16 columns (rows of W) and blocks of 128 values of K: a lane reads 16 bytes, 32 values of one
 // row of W, so four lanes read 64 bytes of a row, and a batch of 4 blocks that follow each other 256: whole
@@ -34,7 +33,7 @@
 //     aligned; sizes where it is not (PER == 0) load one a block.
 //   - Stages of X through registers, 35: copies straight into LDS, which the compiler does not count, made each wait for W one
 //     for the copies behind it.
-//   - Packed subtractions and one addition for each address in LDS, 29.
+//   - Packed subtractions and one addition for each address in LDS, 29.  Now no part left out by itself gains more than 2.
 //
 // Waves of a workgroup stand side by side, or take K in turn where N alone leaves compute units without work; their
 // sums meet in LDS.
@@ -138,15 +137,18 @@ __device__ __forceinline__ void copy16_to_lds_far(__amdgpu_buffer_rsrc_t r, void
     asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" : : "v"(voffset), "s"(r), "{m0}"(m0) : "memory");
 }
 
-constexpr int kWaves = 8;
-constexpr int kDepth = 4;            // blocks of 128 values that a wave has under way: a batch
+// Waves of a workgroup, and blocks of 128 values that each has under way: a batch.  (More than 32 rows leave no
+// room in LDS for a stage of more than 512 values; 16 waves on those took 28.5 us for the case above, 8 took 29.4.)
+constexpr int waves_of(int MT) { return MT > 2 ? 16 : 8; }
+constexpr int depth_of(int MT) { return MT > 2 ? 2 : 4; }
 constexpr int kStageBytes = 64 * 1024;  // of LDS for X, twice
 
 // MT: products of 16 rows.  PER: a scale is for 1, 2 or 4 chunks of 32 (4: or a multiple), K a multiple of 128 and the
 // scales aligned to those of a block; 0: any of the rest.
 // STAGED: X passes through LDS in stages of a batch of each wave; else it is there as a whole.
 template <class T, class TO, bool E2M1, int MT, int PER, bool STAGED>
-__global__ __launch_bounds__(kWaves * 64, 2) void w4_kernel(W4Args a) {
+__global__ __launch_bounds__(waves_of(MT) * 64, waves_of(MT) / 4) void w4_kernel(W4Args a) {
+    constexpr int kWaves = waves_of(MT), kDepth = depth_of(MT);
     typedef Half<T> H;
     typedef typename H::x8 x8;
     constexpr bool EXACT = !E2M1 && std::is_same<T, _Float16>::value;  // zero points leave the elements
@@ -168,7 +170,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void w4_kernel(W4Args a) {
 
     // Scales and zero points.  PER > 0: lane row g4 holds those of a batch's block g4.  PER == 0: of chunk g4 of each
     // block.  Raw: put together where they are used, since that waits for them.
-    constexpr int SB = E2M1 ? 1 : 2, NS = PER > 0 ? 4 / PER : kDepth;
+    constexpr int SB = E2M1 ? 1 : 2, NS = PER > 0 ? 4 / PER : 1;
     struct Scales {
         uint32_t s[PER > 0 ? (NS * SB + 3) / 4 : kDepth];
         uint32_t z[PER > 0 ? 1 : kDepth];
@@ -202,7 +204,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void w4_kernel(W4Args a) {
         }
     };
     // the same through registers, so that the compiler knows how many loads there are in its waits for W
-    constexpr int XC = kStageBytes / 1024 / kWaves, XN = STAGED ? MT == 3 ? 6 : XC : 1;
+    constexpr int XC = kStageBytes / 1024 / kWaves, XN = STAGED ? MT == 3 ? XC * 3 / 4 : XC : 1;
     u32x4_t xs[XN];
     auto stage_load = [&](int s) {
 #pragma unroll
@@ -222,7 +224,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void w4_kernel(W4Args a) {
     };
     // This lane's 16 bytes of chunk y of a block; of a row past the last, any.  KC: a.kc where it is always the same,
     // so that the rows' distance stands in the instructions.
-    constexpr int KC = STAGED && MT > 2 ? 128 * kDepth : 0;
+    constexpr int KC = STAGED && MT > 2 ? 512 : 0;
     const char* xrow[KC > 0 ? 1 : MT];
     int piece[4];
     if constexpr (KC > 0) xrow[0] = lds + r16 * KC * 2;
@@ -357,6 +359,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void w4_kernel(W4Args a) {
 
 template <class T, class TO, bool E2M1, int MT, bool STAGED>
 hipError_t run(const W4Args& a, hipStream_t st) {
+    constexpr int kWaves = waves_of(MT);
     const dim3 grid((a.N + 16 * a.wn - 1) / (16 * a.wn), (a.M + a.rows - 1) / a.rows), wg(kWaves * 64);
     const int x = (STAGED && MT > 2 ? 16 * MT : a.rows) * a.kc * 2 * (STAGED ? 2 : 1), sums = kWaves * MT * 1024;
     const int lds = x > sums ? x : sums;
@@ -378,21 +381,40 @@ hipError_t run(const W4Args& a, hipStream_t st) {
     return hipGetLastError();
 }
 
-template <class T, class TO, bool E2M1>
-hipError_t by_rows(W4Args a, int cus, hipStream_t st) {
-    a.rows = a.M < 64 ? a.M : 64;
+// The rows of a workgroup, its waves side by side and the stages of X; is X there as a whole?
+bool share(W4Args& a, int rows, int cus) {
+    a.rows = rows;
+    if (rows > 32) {
+        a.wn = 8;
+        a.kc = 512;
+        return false;
+    }
     // Waves side by side, as few as leave a workgroup for every compute unit; the others share K.  A stage of X
     // is a batch of each of those, or all of K where it fits.
-    bool staged;
+    constexpr int waves = waves_of(1), batch = 128 * depth_of(1);
     for (a.wn = 1;; a.wn *= 2) {
-        const int kc = 128 * kDepth * (kWaves / a.wn), whole = a.K > 0 ? (a.K + kc - 1) / kc * kc : kc;
-        staged = a.rows > 32 || (int64_t)a.rows * whole * 2 > 2 * kStageBytes;
-        a.kc = staged ? kc : whole;
-        if (a.wn == kWaves || ((!staged || a.rows * kc * 2 <= kStageBytes) && (a.N + 16 * a.wn - 1) / (16 * a.wn) <= 2 * cus)) break;
+        const int kc = batch * (waves / a.wn), all = a.K > 0 ? (a.K + kc - 1) / kc * kc : kc;
+        const bool whole = (int64_t)rows * all * 2 <= 2 * kStageBytes;
+        a.kc = whole ? all : kc;
+        if (a.wn == waves || ((whole || rows * kc * 2 <= kStageBytes) && (a.N + 16 * a.wn - 1) / (16 * a.wn) <= 2 * cus)) return whole;
     }
-    if (a.rows <= 16) return staged ? run<T, TO, E2M1, 1, true>(a, st) : run<T, TO, E2M1, 1, false>(a, st);
-    if (a.rows <= 32) return staged ? run<T, TO, E2M1, 2, true>(a, st) : run<T, TO, E2M1, 2, false>(a, st);
-    return a.rows <= 48 ? run<T, TO, E2M1, 3, true>(a, st) : run<T, TO, E2M1, 4, true>(a, st);
+}
+
+template <class T, class TO, bool E2M1>
+hipError_t by_rows(W4Args a, int cus, hipStream_t st) {
+    // 64 rows to a workgroup, so that the weights pass once; fewer where that leaves more than half of the compute units
+    // without one (the weights come out of a cache after the first time).  bf16, groups of 128, K = 4096: 48 rows,
+    // N = 4096 15.8 us, 25.5 with all rows in each of 32 workgroups; 32 rows, N = 12288 (192 workgroups) 16.2, 23.4 with
+    // 16 rows to each of twice as many.
+    int rows = a.M < 64 ? a.M : 64;
+    bool whole = share(a, rows, cus);
+    while (rows > 16 && (int64_t)((a.N + 16 * a.wn - 1) / (16 * a.wn)) * ((a.M + rows - 1) / rows) < cus / 2) {
+        rows = rows > 32 ? 32 : 16;
+        whole = share(a, rows, cus);
+    }
+    if (rows <= 16) return whole ? run<T, TO, E2M1, 1, false>(a, st) : run<T, TO, E2M1, 1, true>(a, st);
+    if (rows <= 32) return whole ? run<T, TO, E2M1, 2, false>(a, st) : run<T, TO, E2M1, 2, true>(a, st);
+    return rows <= 48 ? run<T, TO, E2M1, 3, true>(a, st) : run<T, TO, E2M1, 4, true>(a, st);
 }
 
 template <class T>
@@ -401,7 +423,8 @@ hipError_t by_type(const W4Args& a, bool e2m1, bool out_f32, int cus, hipStream_
     return out_f32 ? by_rows<T, float, false>(a, cus, st) : by_rows<T, T, false>(a, cus, st);
 }
 
-static_assert(64 * 128 * kDepth * 2 <= kStageBytes, "a stage of 64 rows, for waves side by side");
+static_assert(128 * depth_of(4) * waves_of(4) / 8 == 512 && 64 * 512 * 2 <= kStageBytes && 32 * 128 * depth_of(2) * 2 <= kStageBytes,
+              "a stage of all rows, for waves side by side");
 
 }  // namespace
 

@@ -1,9 +1,10 @@
 """gemm_w4 on the GPU against the float64 oracle.
 
-Tolerance, as the header states it: 2^-17 of sum |x| scale (q + zero) (E2M1: sum |x w|), and the result's
-own rounding.  (Products of 32 values, K / 32 additions of them dealt to at least 4 waves, and those
-to each other: at most 2^7 roundings of 2^-24 for K <= 16384.  The long sums of test_large_offsets
-make 2^10.)
+Tolerance, as the header states it: (K / 32 + 96) 2^-24 of sum |x| scale (q + zero) (E2M1: sum |x w|), and the result's
+own rounding.  (A matrix instruction adds 32 products and its operand, at most 33 roundings of the sizes of its own
+group; a group has two of them for each 32 values, q's and zero's: 66, and 8 more for the sums they join.  The group's
+sum times its scale is rounded once when it is added to those before, K / 32 times at most, whatever waves
+share K, and the 16 waves' sums at most 16 times.)
 """
 import numpy as np
 import pytest
@@ -37,13 +38,14 @@ def make(M, N, K, group=32, elem="u4", zeros=True, dt=BF, seed=0):
 def check(out, x, w, s, z, elem):
     sc = s.cpu().numpy() if elem == "e2m1" else f64(s)
     ref, mag = os_.gemm_w4(f64(x), w.cpu().numpy(), sc, None if z is None else z.cpu().numpy(), elem)
-    tol = 2.0 ** -17 * mag + 1.01 * ol.half_ulp(ref, NAMES[out.dtype])
+    u = (x.shape[1] / 32 + 96) * 2.0 ** -24
+    tol = u * mag + 1.01 * ol.half_ulp(ref, NAMES[out.dtype])
     got = f64(out)
     if out.dtype is HF:
         # fp16 ends at 65504, and what is half a step (16) or more past it rounds to infinity
         past = np.isinf(got)
         assert (np.sign(ref)[past] == np.sign(got)[past]).all() and (np.abs(ref) + tol >= 65520)[past].all()
-        assert past[np.abs(ref) - 2.0 ** -17 * mag >= 65520].all()
+        assert past[np.abs(ref) - u * mag >= 65520].all()
         got = np.where(past, ref, got)
     err = np.abs(got - ref)
     assert (err <= tol).all(), f"worst {np.nanmax(err / tol)} at {np.argwhere(~(err <= tol))[:4]}"
@@ -134,7 +136,8 @@ def test_nothing_to_do():
 
 
 def test_large_offsets():
-    """Weights past 2^32 bytes (67000 columns of 131072 values): the last columns."""
+    """Weights past 2^32 bytes (67000 columns of 131072 values): the last columns.  (Groups of 1024 are added 128
+    values at a time: K / 128 roundings.)"""
     N, K = 67000, 131072
     g = torch.Generator(device=DEV).manual_seed(1)
     w = torch.randint(0, 256, (N, K // 2), generator=g, dtype=torch.uint8, device=DEV)
@@ -143,4 +146,17 @@ def test_large_offsets():
     out = tcm.gemm_w4(x, w, s, out_dtype=F32)
     for n in (0, 32768, 65535, 65536, 66999):
         ref, mag = os_.gemm_w4(f64(x), w[n:n + 1].cpu().numpy(), f64(s[n:n + 1]))
-        assert (np.abs(f64(out[:, n:n + 1]) - ref) <= 2.0 ** -14 * mag).all(), n
+        assert (np.abs(f64(out[:, n:n + 1]) - ref) <= (K / 128 + 96) * 2.0 ** -24 * mag).all(), n
+
+
+# Enough columns that a workgroup takes up to 64 rows, or 32 with X in stages or as a whole
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("M,N,K,group,elem", [
+    (33, 16385, 96, 32, "u4"), (48, 16400, 544, 32, "u4"), (49, 16390, 512, 32, "u4"), (63, 16384, 640, 64, "u4"),
+    (64, 16417, 1152, 64, "u4"), (40, 16393, 1024, 128, "u4"), (65, 16385, 960, 96, "u4"), (64, 16385, 1280, 256, "u4"),
+    (36, 16390, 1056, 32, "e2m1"), (64, 16386, 1152, 32, "e2m1"),
+    (17, 2055, 992, 32, "u4"), (32, 2064, 2048, 64, "u4"), (29, 8193, 2304, 64, "u4"), (32, 8200, 2336, 32, "u4"),
+    (31, 8197, 2304, 32, "e2m1"), (20, 8196, 2432, 128, "u4"), (15, 2050, 4352, 128, "u4"), (16, 4100, 4384, 32, "e2m1")])
+def test_many_columns(M, N, K, group, elem, dt):
+    c = make(M, N, K, group, elem=elem, dt=dt, seed=M)
+    check(tcm.gemm_w4(*c, elem=elem), *c, elem)
