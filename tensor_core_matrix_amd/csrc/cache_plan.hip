@@ -1,15 +1,14 @@
 // Pages and slots for sequences that grow or shrink.
 //
-// Bound by latency: a step touches a few numbers a sequence.  One workgroup does the stack and
-// the table: of 1024 sequences at a time, a lane each, the sums over the sequences before, then
-// the pages, several a lane -- each finds its sequence by bisection of those sums, between the sequences of every 64th page.  Returned
-// pages are all on the stack before the first is taken, and how many there are decides where each goes, so they are gone
-// through twice.  Each wave has one stretch of them, so that it counts and places without a word to the
-// others but its count, and kAtOnce pages a lane, whose bisections and loads are under way together
-// (with one a lane and a sum over all lanes for each 1024 pages, a step that returns 16 thousand pages and takes
-// 12 thousand needed 61 us, now 26).
-// The new tokens' slots follow in the same workgroup while they are few, else in a kernel of
-// their own, whose workgroups do not wait for each other.
+// Bound by latency: a step touches a few numbers a sequence.  One workgroup does the stack and the table: of 1024
+// sequences at a time, a lane each, the sums over the sequences before, then the pages, several a lane -- each
+// finds its sequence by bisection of those sums, between the sequences of every 64th page.  Returned pages are all
+// on the stack before the first is taken, and how many there are decides where each goes, so they are gone through
+// twice.  Each wave has one stretch of them, so that it counts and places without a word to the others but its
+// count, and kAtOnce pages a lane, whose bisections and loads are under way together (with one a lane and a sum
+// over all lanes for each 1024 pages, a step that returns 16 thousand pages and takes 12 thousand needed 61 us, now
+// 26). The new tokens' slots follow in the same workgroup while they are few, else in a kernel of their own, whose
+// workgroups do not wait for each other.
 #include "step_internal.h"
 
 namespace tcm {
@@ -55,8 +54,8 @@ __device__ __forceinline__ int owner(const int64_t* before, int n, int64_t i) {
         if (o + step < n && before[o + step] <= i) o += step;
     return o;
 }
-// The same for the numbers 64 u + lane from i0 on (past the end: the last one): lanes find those of every 64th number,
-// and the others look between them, where there is mostly one sequence or two.
+// The same for the numbers 64 u + lane from i0 on (past the end: the last one): lanes find those of every 64th
+// number, and the others look between them, where there is mostly one sequence or two.
 __device__ __forceinline__ void owners(const int64_t* before, int n, int64_t i0, int64_t end, int64_t* i, int* o) {
     const int lane = threadIdx.x & 63;
     const int edge = owner(before, n, min(i0 + 64 * min(lane, kAtOnce), end - 1));
@@ -114,8 +113,8 @@ __global__ __launch_bounds__(kLanes) void plan_kernel(PlanArgs a) {
         __syncthreads();
         return all;
     };
-    // Goes through this wave's pages of them, in order: put(page or -1, entry or NULL, valid ones of the wave before it);
-    // returns its valid ones.
+    // Goes through this wave's pages of them, in order: put(page or -1, entry or NULL, valid ones of the wave
+    // before it); returns its valid ones.
     auto sweep = [&](int b0, int64_t all, auto put) {
         const int n = min(a.B - b0, kLanes);
         const int64_t per = (all + kLanes - 1) / kLanes * 64, end = min(all, (wave + 1) * per);

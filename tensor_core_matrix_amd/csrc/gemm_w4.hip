@@ -1,10 +1,11 @@
 // Out = X W^T for few rows X and 4-bit weights W.
 //
-// Bound by memory while X has few rows, since every 64 rows pass over the weights once; from about 40 rows on loads, unpacking (about 90
-// vector instructions a block of 16 x 128) and X's way through LDS take about the same time each.  Measured on an MI355X, weights as a rule not in a cache:
+// Bound by memory while X has few rows, since every 64 rows pass over the weights once; from about 40 rows on
+// loads, unpacking (about 90 vector instructions a block of 16 x 128) and X's way through LDS take about the same
+// time each.  Measured on an MI355X, weights as a rule not in a cache:
 //
 //   M   N      K     elements, group, type      us     weights and scales, TB/s
-//   1   4096   4096  U4, 128, zeros, bf16       8.3    1.1  (an empty call of this library takes 7)
+//   1   4096   4096  U4, 128, zeros, bf16       8.3    1.1  (most of it the call itself)
 //   12  12288  4096  E2M1, 32, bf16             14.8   1.8
 //   48  32003  4096  U4, 64, fp16 to fp32       28.5   2.4
 //
@@ -18,22 +19,22 @@
 // other; the four lanes that hold the 128 of a row trade their words (a transposition of
 // 4 x 4 words by register exchanges between rows of lanes) and each gets 8 of every 32.
 //
-// The whole numbers 0 .. 15 are E4M3 bytes times 2^9 as they are -- below 8 the byte is
-// subnormal, q 2^-9, and from 8 on it has exponent 1: (1 + (q - 8) / 8) 2^-6 -- so the
-// conversion of E4M3 pairs gives both 16-bit types exactly.  Zero points are subtracted from elements of fp16, which
-// have packed subtractions; for bf16, which has none, they are a second product with the same X and a constant
-// -zero.  Sums of a group are fp32 and are multiplied by its scale in fp32.  E2M1 elements have a conversion
-// of their own.
+// The whole numbers 0 .. 15 are E4M3 bytes times 2^9 as they are -- below 8 the byte is subnormal, q 2^-9, and from
+// 8 on it has exponent 1: (1 + (q - 8) / 8) 2^-6 -- so the conversion of E4M3 pairs gives both 16-bit types
+// exactly.  Zero points are subtracted from elements of fp16, which have packed subtractions; for bf16, which has
+// none, they are a second product with the same X and a constant -zero.  Sums of a group are fp32 and are
+// multiplied by its scale in fp32.  E2M1 elements have a conversion of their own.
 //
 // What the loads need, found by leaving parts out (the call of 48 rows, 82 us at first):
-//   - X in LDS, once for all waves of a workgroup.  Read by each wave for itself it was the largest part: 66 us, and 35
-//     where all read the same address.  Now 42.
+//   - X in LDS, once for all waves of a workgroup, 42.  Read by each wave for itself it was the largest part: 66,
+//     and 35 where all read the same address.
 //   - No load under a condition: the compiler waits, where two ways meet, for what is certain on both.
 //   - A lane's scales in one load a batch rather than one a block, 37.  So a lane's row of scales has to be
 //     aligned; sizes where it is not (PER == 0) load one a block.
-//   - Stages of X through registers, 35: copies straight into LDS, which the compiler does not count, made each wait for W one
-//     for the copies behind it.
-//   - Packed subtractions and one addition for each address in LDS, 29.  Now no part left out by itself gains more than 2.
+//   - Stages of X through registers, 35: copies straight into LDS, which the compiler does not count, made each wait
+//     for W one for the copies behind it.
+//   - Packed subtractions and one addition for each address in LDS, 29.  Now no part left out by itself gains more
+//     than 2.
 //
 // Waves of a workgroup stand side by side, or take K in turn where N alone leaves compute units without work; their
 // sums meet in LDS.
@@ -133,7 +134,8 @@ __device__ __forceinline__ typename Half<T>::x8 splat(float x) {
 
 // (as in the attention of drafted tokens: the resource may come out of vector registers)
 __device__ __forceinline__ void copy16_to_lds_far(__amdgpu_buffer_rsrc_t r, void* lds_wave_base, uint32_t voffset) {
-    const uint32_t m0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds_wave_base);
+    const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds_wave_base;
+    const uint32_t m0 = __builtin_amdgcn_readfirstlane(at);
     asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" : : "v"(voffset), "s"(r), "{m0}"(m0) : "memory");
 }
 
@@ -143,9 +145,9 @@ constexpr int waves_of(int MT) { return MT > 2 ? 16 : 8; }
 constexpr int depth_of(int MT) { return MT > 2 ? 2 : 4; }
 constexpr int kStageBytes = 64 * 1024;  // of LDS for X, twice
 
-// MT: products of 16 rows.  PER: a scale is for 1, 2 or 4 chunks of 32 (4: or a multiple), K a multiple of 128 and the
-// scales aligned to those of a block; 0: any of the rest.
-// STAGED: X passes through LDS in stages of a batch of each wave; else it is there as a whole.
+// MT: products of 16 rows.  PER: a scale is for 1, 2 or 4 chunks of 32 (4: or a multiple), K a multiple of 128 and
+// the scales aligned to those of a block; 0: any of the rest. STAGED: X passes through LDS in stages of a batch of
+// each wave; else it is there as a whole.
 template <class T, class TO, bool E2M1, int MT, int PER, bool STAGED>
 __global__ __launch_bounds__(waves_of(MT) * 64, waves_of(MT) / 4) void w4_kernel(W4Args a) {
     constexpr int kWaves = waves_of(MT), kDepth = depth_of(MT);
@@ -168,8 +170,8 @@ __global__ __launch_bounds__(waves_of(MT) * 64, waves_of(MT) / 4) void w4_kernel
     const uint8_t* const zeros = a.zeros ? a.zeros : (const uint8_t*)a.scales;
     auto load = [&](int block) { return wr[min(4 * block + g4, chunks - 1)]; };  // (chunks past the end are not used)
 
-    // Scales and zero points.  PER > 0: lane row g4 holds those of a batch's block g4.  PER == 0: of chunk g4 of each
-    // block.  Raw: put together where they are used, since that waits for them.
+    // Scales and zero points.  PER > 0: lane row g4 holds those of a batch's block g4.  PER == 0: of chunk g4 of
+    // each block.  Raw: put together where they are used, since that waits for them.
     constexpr int SB = E2M1 ? 1 : 2, NS = PER > 0 ? 4 / PER : 1;
     struct Scales {
         uint32_t s[PER > 0 ? (NS * SB + 3) / 4 : kDepth];
@@ -192,8 +194,8 @@ __global__ __launch_bounds__(waves_of(MT) * 64, waves_of(MT) / 4) void w4_kernel
         }
     };
 
-    // X: stages of a.kc values of every row.  A row's 16-byte piece c lies at c ^ (row % 16), so that the 16 rows of
-    // an operand meet different banks.
+    // X: stages of a.kc values of every row.  A row's 16-byte piece c lies at c ^ (row % 16), so that the 16 rows
+    // of an operand meet different banks.
     const int stage_bytes = (STAGED && MT > 2 ? 16 * MT : rows) * a.kc * 2, pieces = a.kc / 8;
     auto stage = [&](int s, int buffer) {
         // 64 pieces a copy, dealt to the waves; what lies past a row's end is zero
@@ -211,7 +213,8 @@ __global__ __launch_bounds__(waves_of(MT) * 64, waves_of(MT) / 4) void w4_kernel
         for (int j = 0; j < XN; ++j) {
             const int i = min(wave + kWaves * j, rows * pieces / 64 - 1);
             const int row = i / (pieces / 64), c = i % (pieces / 64) * 64 + lane;
-            xs[j] = __builtin_amdgcn_raw_buffer_load_b128(make_rsrc((const T*)a.x + (int64_t)(m0 + row) * a.ldx, (uint32_t)a.K * 2),
+            const T* const from = (const T*)a.x + (int64_t)(m0 + row) * a.ldx;
+            xs[j] = __builtin_amdgcn_raw_buffer_load_b128(make_rsrc(from, (uint32_t)a.K * 2),
                                                           (uint32_t)(s * a.kc + (c ^ (row & 15)) * 8) * 2, 0, 0);
         }
     };
@@ -222,8 +225,8 @@ __global__ __launch_bounds__(waves_of(MT) * 64, waves_of(MT) / 4) void w4_kernel
             if (i < rows * pieces / 64) *(u32x4_t*)(lds + buffer * stage_bytes + i * 1024 + lane * 16) = xs[j];
         }
     };
-    // This lane's 16 bytes of chunk y of a block; of a row past the last, any.  KC: a.kc where it is always the same,
-    // so that the rows' distance stands in the instructions.
+    // This lane's 16 bytes of chunk y of a block; of a row past the last, any.  KC: a.kc where it is always the
+    // same, so that the rows' distance stands in the instructions.
     constexpr int KC = STAGED && MT > 2 ? 512 : 0;
     const char* xrow[KC > 0 ? 1 : MT];
     int piece[4];
@@ -241,8 +244,8 @@ __global__ __launch_bounds__(waves_of(MT) * 64, waves_of(MT) / 4) void w4_kernel
     f32x4_t acc[MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i) acc[i] = (f32x4_t){};
-    // at: the block's first byte in a row of X's stage; left: its chunks, 4 (but for a row's last block); s, z: words that hold
-    // the scales and zero points, one a chunk (PER == 0) or those of the block
+    // at: the block's first byte in a row of X's stage; left: its chunks, 4 (but for a row's last block); s, z:
+    // words that hold the scales and zero points, one a chunk (PER == 0) or those of the block
     auto compute = [&](u32x4_t w, const uint32_t* s, const uint32_t* z, int at, int left) {
         turn(w);
         f32x4_t p[MT];
@@ -396,16 +399,17 @@ bool share(W4Args& a, int rows, int cus) {
         const int kc = batch * (waves / a.wn), all = a.K > 0 ? (a.K + kc - 1) / kc * kc : kc;
         const bool whole = (int64_t)rows * all * 2 <= 2 * kStageBytes;
         a.kc = whole ? all : kc;
-        if (a.wn == waves || ((whole || rows * kc * 2 <= kStageBytes) && (a.N + 16 * a.wn - 1) / (16 * a.wn) <= 2 * cus)) return whole;
+        const bool fits = whole || rows * kc * 2 <= kStageBytes;
+        if (a.wn == waves || (fits && (a.N + 16 * a.wn - 1) / (16 * a.wn) <= 2 * cus)) return whole;
     }
 }
 
 template <class T, class TO, bool E2M1>
 hipError_t by_rows(W4Args a, int cus, hipStream_t st) {
-    // 64 rows to a workgroup, so that the weights pass once; fewer where that leaves more than half of the compute units
-    // without one (the weights come out of a cache after the first time).  bf16, groups of 128, K = 4096: 48 rows,
-    // N = 4096 15.8 us, 25.5 with all rows in each of 32 workgroups; 32 rows, N = 12288 (192 workgroups) 16.2, 23.4 with
-    // 16 rows to each of twice as many.
+    // 64 rows to a workgroup, so that the weights pass once; fewer where that leaves more than half of the compute
+    // units without one (the weights come out of a cache after the first time).  bf16, groups of 128, K = 4096: 48
+    // rows, N = 4096 15.8 us, 25.5 with all rows in each of 32 workgroups; 32 rows, N = 12288 (192 workgroups)
+    // 16.2, 23.4 with 16 rows to each of twice as many.
     int rows = a.M < 64 ? a.M : 64;
     bool whole = share(a, rows, cus);
     while (rows > 16 && (int64_t)((a.N + 16 * a.wn - 1) / (16 * a.wn)) * ((a.M + rows - 1) / rows) < cus / 2) {
@@ -423,7 +427,8 @@ hipError_t by_type(const W4Args& a, bool e2m1, bool out_f32, int cus, hipStream_
     return out_f32 ? by_rows<T, float, false>(a, cus, st) : by_rows<T, T, false>(a, cus, st);
 }
 
-static_assert(128 * depth_of(4) * waves_of(4) / 8 == 512 && 64 * 512 * 2 <= kStageBytes && 32 * 128 * depth_of(2) * 2 <= kStageBytes,
+static_assert(128 * depth_of(4) * waves_of(4) / 8 == 512 && 64 * 512 * 2 <= kStageBytes &&
+                  32 * 128 * depth_of(2) * 2 <= kStageBytes,
               "a stage of all rows, for waves side by side");
 
 }  // namespace

@@ -120,7 +120,8 @@ __global__ __launch_bounds__(L > 256 ? L : 256) void norm_kernel(NormArgs a) {
     int turn = 0;
     // (a launch ends at 2^32 threads, so workgroups go on where rows are left; those of more
     // than a wave take one row at a time)
-    for (int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / L; row < a.T; row += (int64_t)gridDim.x * ROWS, turn ^= 1) {
+    const int64_t first = (int64_t)blockIdx.x * ROWS + threadIdx.x / L;
+    for (int64_t row = first; row < a.T; row += (int64_t)gridDim.x * ROWS, turn ^= 1) {
         const T* x = (const T*)a.x + row * a.ldx;
         const T* r = (const T*)a.r + row * a.ldr;
         float v[P][8];
@@ -162,11 +163,11 @@ __global__ __launch_bounds__(L > 256 ? L : 256) void norm_kernel(NormArgs a) {
     }
 }
 
-// A workgroup takes rows blockIdx.x, + gridDim.x, .. with L lanes each; a lane's columns are the same in
-// every row, so it sums their weight gradients in registers.  Where there is room (P < 4) the next row is
-// on its way while this one is worked on, and the weights stay too: of the next row nobody has written anything, also
-// where dX is an operand, since rows are one workgroup's.  8192 x 4096 with dsum, bf16: 50 us, 5.4 TB/s, and 4.7 for the sum of the
-// partial sums (75 and 10 with loads when they are needed and 64 workgroups for the sum).
+// A workgroup takes rows blockIdx.x, + gridDim.x, .. with L lanes each; a lane's columns are the same in every row,
+// so it sums their weight gradients in registers.  Where there is room (P < 4) the next row is on its way while
+// this one is worked on, and the weights stay too: of the next row nobody has written anything, also where dX is an
+// operand, since rows are one workgroup's.  8192 x 4096 with dsum, bf16: 50 us, 5.4 TB/s, and 4.7 for the sum of
+// the partial sums (75 and 10 with loads when they are needed and 64 workgroups for the sum).
 template <class T, int L, int P, bool DW, bool R>
 __global__ __launch_bounds__(L) void norm_bwd_kernel(NormArgs a) {
     typedef typename Piece<T>::type x8;
@@ -293,7 +294,8 @@ hipError_t by_dim(const NormArgs& a, hipStream_t st) {
 
 template <class T>
 hipError_t by_out(const NormArgs& a, NormOut out, hipStream_t st) {
-    return out == kNormHalf ? by_dim<T, kNormHalf>(a, st) : out == kNormF32 ? by_dim<T, kNormF32>(a, st) : by_dim<T, kNormMx>(a, st);
+    if (out == kNormHalf) return by_dim<T, kNormHalf>(a, st);
+    return out == kNormF32 ? by_dim<T, kNormF32>(a, st) : by_dim<T, kNormMx>(a, st);
 }
 
 template <class T, int L, int P>

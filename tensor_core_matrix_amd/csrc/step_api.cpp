@@ -333,9 +333,9 @@ tcm_status tcm_paged_tree_attention(const tcm_heads* q, const tcm_cache* cache,
     a.D = (int32_t)D;
     a.pages = (int32_t)cache->pages;
     a.page_size = (int32_t)cache->page_size;
-    // With 2^s >= page_size the first power of two, m = floor(2^(31 + s) / page_size) + 1 is at most
-    // 2^(31 + s) / page_size + 1, so n m is past n 2^(31 + s) / page_size by at most n < 2^31 <= 2^(31 + s) / page_size
-    // (and m < 2^32): the quotient's whole part is right.
+    // With 2^s >= page_size the first power of two, m = floor(2^(31 + s) / page_size) + 1 is at most 2^(31 + s) /
+    // page_size + 1, so n m is past n 2^(31 + s) / page_size by at most n < 2^31 <= 2^(31 + s) / page_size (and m <
+    // 2^32): the quotient's whole part is right.
     int s2 = 0;
     while ((int64_t(1) << s2) < cache->page_size) ++s2;
     a.page_magic = (uint32_t)((uint64_t(1) << (31 + s2)) / (uint64_t)cache->page_size + 1);

@@ -218,7 +218,9 @@ struct TreeShape {
 // DP: D rounded up to 64, 128 or 256.  ALIGNED: page_size is a multiple of 16, so 16 keys from a multiple
 // of 16 on lie in one page.
 template <class T, int DP, bool E4M3, bool ALIGNED, int WR, int RB>
-__global__ __launch_bounds__((TreeShape<DP, E4M3, WR, RB>::WAVES * 64), (DP > 128 || TreeShape<DP, E4M3, WR, RB>::LDS > 72 * 1024 ? 1 : 2)) void tree_kernel(TreeArgs p) {
+__global__ __launch_bounds__((TreeShape<DP, E4M3, WR, RB>::WAVES * 64),
+                             (DP > 128 || TreeShape<DP, E4M3, WR, RB>::LDS > 72 * 1024 ? 1 : 2))
+void tree_kernel(TreeArgs p) {
     typedef TreeShape<DP, E4M3, WR, RB> S;
     typedef Half16<T> H;
     typedef typename H::x8 x8;
@@ -259,584 +261,589 @@ __global__ __launch_bounds__((TreeShape<DP, E4M3, WR, RB>::WAVES * 64), (DP > 12
     }
     TreePlace place = tree_place(p, ROUND, step, lanes);
     for (bool head = true;; head = false) {
-    const TreeUnit unit = tree_unit(place, step);
-    const int b = place.b, hk = unit.hk, blk = unit.blk;
-    // the tiles [tile0, tile1) of the block, of place.tiles
-    const int64_t tile_step = unit.first + kTreeSetup, past = unit.first + kTreeSetup + place.tiles;
-    const int tile0 = (int)max(step - tile_step, (int64_t)0), tile1 = (int)(min(stop, past) - tile_step);
-    if (head && p.split && threadIdx.x == 0) {
-        // A block whose first tiles are the stretch's before this one: its parts are this one's to announce.
-        TreeSplit s = {0, b, hk, blk};
-        if (step > tile_step && share.owner(tile_step) == w - 1) s.parts = share.owner(past - 1) - w + 2;
-        p.split[w] = s;
-    }
-    if (tile1 > 0) {
-    const bool part = tile1 - tile0 < place.tiles;
-    // this stretch's first or last part of a block
-    const int64_t slot = 2 * (int64_t)w + (tile0 == 0);
-    const TreeRange rg = tree_range(p, b, blk);
-    // the keys [start, end) of it
-    const int64_t from = rg.base + (int64_t)tile0 * ROUND;
-    const int start = (int)max(from, (int64_t)(rg.base + (rg.lo - rg.base) / ROUND * ROUND));
-    const int end = (int)min((int64_t)rg.end, rg.base + (int64_t)tile1 * ROUND);
-
-    // this lane's rows (those past the last are the last, with zeros for q, and not stored)
-    const int row0 = blk * S::ROWS + wr * 16 * RB;
-    const int rows = rg.m * p.G - row0;  // of this wave and the later ones
-    int tok[RB], qhead[RB];
-#pragma unroll
-    for (int i = 0; i < RB; ++i) {
-        const int row = row0 + min(16 * i + r16, rows - 1);
-        tok[i] = row / p.G;
-        qhead[i] = hk * p.G + row - tok[i] * p.G;
-    }
-
-    // ---- keys and values into LDS ---------------------------------------------------
-    // A key's 16-byte piece c lies in LDS at c ^ swz(key), so that the 16 keys of an operand read
-    // meet different banks; swz goes by the key's number within 16.
-    constexpr int SH = KL >= 16 ? 0 : KL == 8 ? 1 : 2;
-    auto swz = [](int key) { return (key >> SH) & ((KL < 16 ? KL : 16) - 1); };
-    char* const stages = lds + wk * 2 * S::STAGE;  // a stage: KT keys, KT values
-    const int kc = lane % KL, kr = lane / KL;
-    const int32_t* const trow = p.table + b * p.table_stride;
-    const char* const kh = p.kc + hk * p.k_head;
-    const char* const vh = p.vc + hk * p.v_head;
-    auto page_of = [&](int key) { return (int)((uint64_t)(uint32_t)key * p.page_magic >> p.page_shift); };
-    struct Tile {
-        int key0;
-        int page[NH];       // ALIGNED: of the 16 keys that the wave copies; else [0] of key l % KT of lane l
-        int entry[NH];      // and their numbers in the table's row
-        uint32_t good[NT];  // the keys that can be used at all (ALIGNED, shared stages: but for their pages)
-    };
-    auto look = [&](int key0) {
-        Tile t;
-        t.key0 = key0;
-        if constexpr (ALIGNED) {
-#pragma unroll
-            for (int y = 0; y < NH; ++y) {
-                const int key = key0 + 16 * (WR > 1 ? wr : y);
-                t.entry[y] = page_of(key);
-                t.page[y] = key < end ? trow[t.entry[y]] : -1;
-            }
-        } else {
-            const int key = key0 + (lane & (KT - 1));
-            t.entry[0] = page_of(key);
-            t.page[0] = key >= rg.lo && key < end ? trow[t.entry[0]] : -1;
+        const TreeUnit unit = tree_unit(place, step);
+        const int b = place.b, hk = unit.hk, blk = unit.blk;
+        // the tiles [tile0, tile1) of the block, of place.tiles
+        const int64_t tile_step = unit.first + kTreeSetup, past = unit.first + kTreeSetup + place.tiles;
+        const int tile0 = (int)max(step - tile_step, (int64_t)0), tile1 = (int)(min(stop, past) - tile_step);
+        if (head && p.split && threadIdx.x == 0) {
+            // A block whose first tiles are the stretch's before this one: its parts are this one's to announce.
+            TreeSplit s = {0, b, hk, blk};
+            if (step > tile_step && share.owner(tile_step) == w - 1) s.parts = share.owner(past - 1) - w + 2;
+            p.split[w] = s;
         }
-        return t;
-    };
-    // ALIGNED: a lane's offsets from the first of 16 keys (16 token strides are less than 2^31 bytes)
-    uint32_t koff[HALF], voff[HALF];
+        if (tile1 > 0) {
+            const bool part = tile1 - tile0 < place.tiles;
+            // this stretch's first or last part of a block
+            const int64_t slot = 2 * (int64_t)w + (tile0 == 0);
+            const TreeRange rg = tree_range(p, b, blk);
+            // the keys [start, end) of it
+            const int64_t from = rg.base + (int64_t)tile0 * ROUND;
+            const int start = (int)max(from, (int64_t)(rg.base + (rg.lo - rg.base) / ROUND * ROUND));
+            const int end = (int)min((int64_t)rg.end, rg.base + (int64_t)tile1 * ROUND);
+
+            // this lane's rows (those past the last are the last, with zeros for q, and not stored)
+            const int row0 = blk * S::ROWS + wr * 16 * RB;
+            const int rows = rg.m * p.G - row0;  // of this wave and the later ones
+            int tok[RB], qhead[RB];
 #pragma unroll
-    for (int q = 0; q < HALF; ++q) {
-        const int key = q * KN + kr, piece = kc ^ swz(key);
-        const bool in = 16 * piece < p.D * ES;
-        koff[q] = in ? key * (uint32_t)p.k_tok + piece * 16 : kOutOfRange;
-        voff[q] = in ? key * (uint32_t)p.v_tok + piece * 16 : kOutOfRange;
-    }
-    u32x4_t held[ALIGNED ? 1 : 2 * NH * HALF];
-    // A wave's copies of a tile, 2 NH HALF of them.  The memory pipe takes one in 16 cycles and more, and a wave that
-    // asks for the next one waits; so those of a whole tile are spread over the products before.
-    struct Copies {
-        __amdgpu_buffer_rsrc_t rk[NH], rv[NH];
-        char* to[NH];
-    };
-    auto copy = [&](const Copies& c, int i) {
-        const int y = i / (2 * HALF), q = i % HALF;
-        if (i / HALF % 2 == 0) copy16_to_lds_far(c.rk[y], c.to[y] + q * 1024, koff[q]);
-        else copy16_to_lds_far(c.rv[y], c.to[y] + KT * KB + q * 1024, voff[q]);
-    };
-    // Asks for a tile; false if its copies are left to the caller.
-    auto issue = [&](Tile& t, int stage, bool leave, Copies& c) {
-        if constexpr (ALIGNED) {
-            const bool whole = t.key0 >= rg.lo && t.key0 + KT <= end;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) t.good[n] = whole ? ~0u : bits_from(rg.lo - t.key0 - 32 * n) & ~bits_from(end - t.key0 - 32 * n);
-#pragma unroll
-            for (int y = 0; y < NH; ++y) {
-                const int h = WR > 1 ? wr : y;
-                const uint32_t found = __builtin_amdgcn_readfirstlane(t.page[y]);
-                const bool is = found < (uint32_t)p.pages;
-                if constexpr (WR > 1) there_[stage][wr] = is ? 0xffffu << (wr & 1) * 16 : 0u;
-                else if (!is) t.good[0] &= h ? 0x0000ffffu : 0xffff0000u;
-                const uint32_t size = is ? kOutOfRange : 0u, page = is ? found : 0;
-                const uint32_t at = t.key0 + 16 * h - t.entry[y] * p.page_size;
-                c.rk[y] = make_rsrc(kh + (page * (uint64_t)p.k_page + at * (uint64_t)p.k_tok), size);
-                c.rv[y] = make_rsrc(vh + (page * (uint64_t)p.v_page + at * (uint64_t)p.v_tok), size);
-                c.to[y] = stages + stage * S::STAGE + h * 16 * KB;
+            for (int i = 0; i < RB; ++i) {
+                const int row = row0 + min(16 * i + r16, rows - 1);
+                tok[i] = row / p.G;
+                qhead[i] = hk * p.G + row - tok[i] * p.G;
             }
-            if (whole) {
-                if (leave) return false;
+
+            // ---- keys and values into LDS ---------------------------------------------------
+            // A key's 16-byte piece c lies in LDS at c ^ swz(key), so that the 16 keys of an operand read
+            // meet different banks; swz goes by the key's number within 16.
+            constexpr int SH = KL >= 16 ? 0 : KL == 8 ? 1 : 2;
+            auto swz = [](int key) { return (key >> SH) & ((KL < 16 ? KL : 16) - 1); };
+            char* const stages = lds + wk * 2 * S::STAGE;  // a stage: KT keys, KT values
+            const int kc = lane % KL, kr = lane / KL;
+            const int32_t* const trow = p.table + b * p.table_stride;
+            const char* const kh = p.kc + hk * p.k_head;
+            const char* const vh = p.vc + hk * p.v_head;
+            auto page_of = [&](int key) { return (int)((uint64_t)(uint32_t)key * p.page_magic >> p.page_shift); };
+            struct Tile {
+                int key0;
+                int page[NH];       // ALIGNED: of the 16 keys that the wave copies; else [0] of key l % KT of lane l
+                int entry[NH];      // and their numbers in the table's row
+                uint32_t good[NT];  // the keys that can be used at all (ALIGNED, shared stages: but for their pages)
+            };
+            auto look = [&](int key0) {
+                Tile t;
+                t.key0 = key0;
+                if constexpr (ALIGNED) {
 #pragma unroll
-                for (int i = 0; i < 2 * NH * HALF; ++i) copy(c, i);
-            } else {
-#pragma unroll
-                for (int y = 0; y < NH; ++y)
-#pragma unroll
-                    for (int q = 0; q < HALF; ++q) {
-                        const int k = t.key0 + 16 * (WR > 1 ? wr : y) + q * KN + kr;
-                        const bool in = k >= rg.lo && k < end;
-                        copy16_to_lds_far(c.rk[y], c.to[y] + q * 1024, in ? koff[q] : kOutOfRange);
-                        copy16_to_lds_far(c.rv[y], c.to[y] + KT * KB + q * 1024, in ? voff[q] : kOutOfRange);
+                    for (int y = 0; y < NH; ++y) {
+                        const int key = key0 + 16 * (WR > 1 ? wr : y);
+                        t.entry[y] = page_of(key);
+                        t.page[y] = key < end ? trow[t.entry[y]] : -1;
                     }
+                } else {
+                    const int key = key0 + (lane & (KT - 1));
+                    t.entry[0] = page_of(key);
+                    t.page[0] = key >= rg.lo && key < end ? trow[t.entry[0]] : -1;
+                }
+                return t;
+            };
+            // ALIGNED: a lane's offsets from the first of 16 keys (16 token strides are less than 2^31 bytes)
+            uint32_t koff[HALF], voff[HALF];
+#pragma unroll
+            for (int q = 0; q < HALF; ++q) {
+                const int key = q * KN + kr, piece = kc ^ swz(key);
+                const bool in = 16 * piece < p.D * ES;
+                koff[q] = in ? key * (uint32_t)p.k_tok + piece * 16 : kOutOfRange;
+                voff[q] = in ? key * (uint32_t)p.v_tok + piece * 16 : kOutOfRange;
             }
-        } else {
-            const bool ok = (uint32_t)t.page[0] < (uint32_t)p.pages;
-            if (!ok) t.page[0] = -1;
-            const uint64_t all = __ballot(ok);
+            u32x4_t held[ALIGNED ? 1 : 2 * NH * HALF];
+            // A wave's copies of a tile, 2 NH HALF of them.  The memory pipe takes one in 16 cycles and more, and a
+            // wave that asks for the next one waits; so those of a whole tile are spread over the products before.
+            struct Copies {
+                __amdgpu_buffer_rsrc_t rk[NH], rv[NH];
+                char* to[NH];
+            };
+            auto copy = [&](const Copies& c, int i) {
+                const int y = i / (2 * HALF), q = i % HALF;
+                if (i / HALF % 2 == 0) copy16_to_lds_far(c.rk[y], c.to[y] + q * 1024, koff[q]);
+                else copy16_to_lds_far(c.rv[y], c.to[y] + KT * KB + q * 1024, voff[q]);
+            };
+            // Asks for a tile; false if its copies are left to the caller.
+            auto issue = [&](Tile& t, int stage, bool leave, Copies& c) {
+                if constexpr (ALIGNED) {
+                    const bool whole = t.key0 >= rg.lo && t.key0 + KT <= end;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) t.good[n] = (uint32_t)(all >> 32 * n);
+                    for (int n = 0; n < NT; ++n) {
+                        const int k = t.key0 + 32 * n;
+                        t.good[n] = whole ? ~0u : bits_from(rg.lo - k) & ~bits_from(end - k);
+                    }
 #pragma unroll
-            for (int y = 0; y < NH; ++y)
+                    for (int y = 0; y < NH; ++y) {
+                        const int h = WR > 1 ? wr : y;
+                        const uint32_t found = __builtin_amdgcn_readfirstlane(t.page[y]);
+                        const bool is = found < (uint32_t)p.pages;
+                        if constexpr (WR > 1) there_[stage][wr] = is ? 0xffffu << (wr & 1) * 16 : 0u;
+                        else if (!is) t.good[0] &= h ? 0x0000ffffu : 0xffff0000u;
+                        const uint32_t size = is ? kOutOfRange : 0u, page = is ? found : 0;
+                        const uint32_t at = t.key0 + 16 * h - t.entry[y] * p.page_size;
+                        c.rk[y] = make_rsrc(kh + (page * (uint64_t)p.k_page + at * (uint64_t)p.k_tok), size);
+                        c.rv[y] = make_rsrc(vh + (page * (uint64_t)p.v_page + at * (uint64_t)p.v_tok), size);
+                        c.to[y] = stages + stage * S::STAGE + h * 16 * KB;
+                    }
+                    if (whole) {
+                        if (leave) return false;
 #pragma unroll
-                for (int q = 0; q < HALF; ++q) {
-                    const int key = (WR > 1 ? wr : y) * 16 + q * KN + kr, piece = kc ^ swz(key & 15);
-                    const int page = __shfl(t.page[0], key), at = t.key0 + key - __shfl(t.entry[0], key) * p.page_size;
-                    u32x4_t& k = held[2 * (y * HALF + q)];
-                    u32x4_t& v = held[2 * (y * HALF + q) + 1];
-                    k = v = (u32x4_t){};
-                    if (page >= 0 && 16 * piece < p.D * ES) {
-                        k = *(const u32x4_t*)(kh + page * p.k_page + at * p.k_tok + piece * 16);
-                        v = *(const u32x4_t*)(vh + page * p.v_page + at * p.v_tok + piece * 16);
+                        for (int i = 0; i < 2 * NH * HALF; ++i) copy(c, i);
+                    } else {
+#pragma unroll
+                        for (int y = 0; y < NH; ++y)
+#pragma unroll
+                            for (int q = 0; q < HALF; ++q) {
+                                const int k = t.key0 + 16 * (WR > 1 ? wr : y) + q * KN + kr;
+                                const bool in = k >= rg.lo && k < end;
+                                copy16_to_lds_far(c.rk[y], c.to[y] + q * 1024, in ? koff[q] : kOutOfRange);
+                                copy16_to_lds_far(c.rv[y], c.to[y] + KT * KB + q * 1024, in ? voff[q] : kOutOfRange);
+                            }
+                    }
+                } else {
+                    const bool ok = (uint32_t)t.page[0] < (uint32_t)p.pages;
+                    if (!ok) t.page[0] = -1;
+                    const uint64_t all = __ballot(ok);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) t.good[n] = (uint32_t)(all >> 32 * n);
+#pragma unroll
+                    for (int y = 0; y < NH; ++y)
+#pragma unroll
+                        for (int q = 0; q < HALF; ++q) {
+                            const int key = (WR > 1 ? wr : y) * 16 + q * KN + kr, piece = kc ^ swz(key & 15);
+                            const int page = __shfl(t.page[0], key), at = t.key0 + key - __shfl(t.entry[0], key) * p.page_size;
+                            u32x4_t& k = held[2 * (y * HALF + q)];
+                            u32x4_t& v = held[2 * (y * HALF + q) + 1];
+                            k = v = (u32x4_t){};
+                            if (page >= 0 && 16 * piece < p.D * ES) {
+                                k = *(const u32x4_t*)(kh + page * p.k_page + at * p.k_tok + piece * 16);
+                                v = *(const u32x4_t*)(vh + page * p.v_page + at * p.v_tok + piece * 16);
+                            }
+                        }
+                }
+                return true;
+            };
+            // what issue() left in registers
+            auto settle = [&](int stage) {
+                if constexpr (!ALIGNED) {
+#pragma unroll
+                    for (int y = 0; y < NH; ++y)
+#pragma unroll
+                        for (int q = 0; q < HALF; ++q) {
+                            char* const to = stages + stage * S::STAGE + (WR > 1 ? wr : y) * 16 * KB + q * 1024 + lane * 16;
+                            *(u32x4_t*)to = held[2 * (y * HALF + q)];
+                            *(u32x4_t*)(to + KT * KB) = held[2 * (y * HALF + q) + 1];
+                        }
+                }
+            };
+
+            // ---- the tiles of this group of waves ---------------------------------------------- Tile r + 1 is
+            // asked for while tile r is computed; its pages were looked up a tile before, by loads that the wait
+            // for tile r's copies covers.  (A scalar load's wait would be the next one for an operand from LDS,
+            // since both have one counter.)
+            const int first = start + KT * wk;
+            const int tiles = first < end ? (end - first + ROUND - 1) / ROUND : 0;
+            Tile tile = look(first);
+            Tile next = look(first + ROUND);
+
+            // Q as the second operand: lane l holds row l % 16 and 8 elements of each step.  Elements of step
+            // s: 32 s + 8 g .. + 7; for E4M3 keys, whose 16-byte pieces cover two steps,
+            // 64 (s / 2) + 16 g + 8 (s % 2) .. + 7.  A negative scale is q's sign (a scale of 0 the least there is:
+            // masked scores are -infinity times it).
+            const float scale = fmaxf(fabsf(p.scale_log2), 0x1p-126f);
+            x8 qf[RB][STEPS];
+#pragma unroll
+            for (int i = 0; i < RB; ++i) {
+                const T* row = (const T*)p.q.p + (int64_t)(rg.row0 + tok[i]) * p.q.ts + (int64_t)qhead[i] * p.q.hs;
+#pragma unroll
+                for (int s = 0; s < STEPS; ++s) {
+                    const int e = E4M3 ? 64 * (s >> 1) + 16 * g4 + 8 * (s & 1) : 32 * s + 8 * g4;
+                    qf[i][s] = 16 * i + r16 < rows && e < p.D ? *(const x8*)(row + e) : (x8){};
+                }
+            }
+            Copies copies;
+            if (tiles > 0) issue(tile, 0, false, copies);
+            // The first key of the context that a row sees (a chain: of all keys)
+            int low[RB];
+#pragma unroll
+            for (int i = 0; i < RB; ++i) {
+                low[i] = 0;
+                if (p.window > 0) {
+                    if (p.tree) {
+                        const uint32_t* w = p.tree + (int64_t)(rg.row0 + tok[i]) * p.tree_words;
+                        int d = 0;
+                        for (int x = 0; x < p.tree_words && 32 * x < rg.all; ++x)
+                            d += __builtin_popcount(w[x] & ~bits_from(rg.all - 32 * x));
+                        low[i] = min(rg.context + d - p.window, rg.context);
+                    } else {
+                        low[i] = rg.context + tok[i] - p.window + 1;
                     }
                 }
-        }
-        return true;
-    };
-    // what issue() left in registers
-    auto settle = [&](int stage) {
-        if constexpr (!ALIGNED) {
-#pragma unroll
-            for (int y = 0; y < NH; ++y)
-#pragma unroll
-                for (int q = 0; q < HALF; ++q) {
-                    char* const to = stages + stage * S::STAGE + (WR > 1 ? wr : y) * 16 * KB + q * 1024 + lane * 16;
-                    *(u32x4_t*)to = held[2 * (y * HALF + q)];
-                    *(u32x4_t*)(to + KT * KB) = held[2 * (y * HALF + q) + 1];
-                }
-        }
-    };
-
-    // ---- the tiles of this group of waves ----------------------------------------------
-    // Tile r + 1 is asked for while tile r is computed; its pages were looked up a tile before, by loads that
-    // the wait for tile r's copies covers.  (A scalar load's wait would be the next one for an operand from
-    // LDS, since both have one counter.)
-    const int first = start + KT * wk;
-    const int tiles = first < end ? (end - first + ROUND - 1) / ROUND : 0;
-    Tile tile = look(first);
-    Tile next = look(first + ROUND);
-
-    // Q as the second operand: lane l holds row l % 16 and 8 elements of each step.  Elements of step
-    // s: 32 s + 8 g .. + 7; for E4M3 keys, whose 16-byte pieces cover two steps,
-    // 64 (s / 2) + 16 g + 8 (s % 2) .. + 7.  A negative scale is q's sign (a scale of 0 the least there is:
-    // masked scores are -infinity times it).
-    const float scale = fmaxf(fabsf(p.scale_log2), 0x1p-126f);
-    x8 qf[RB][STEPS];
-#pragma unroll
-    for (int i = 0; i < RB; ++i) {
-        const T* row = (const T*)p.q.p + (int64_t)(rg.row0 + tok[i]) * p.q.ts + (int64_t)qhead[i] * p.q.hs;
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-            const int e = E4M3 ? 64 * (s >> 1) + 16 * g4 + 8 * (s & 1) : 32 * s + 8 * g4;
-            qf[i][s] = 16 * i + r16 < rows && e < p.D ? *(const x8*)(row + e) : (x8){};
-        }
-    }
-    Copies copies;
-    if (tiles > 0) issue(tile, 0, false, copies);
-    // The first key of the context that a row sees (a chain: of all keys)
-    int low[RB];
-#pragma unroll
-    for (int i = 0; i < RB; ++i) {
-        low[i] = 0;
-        if (p.window > 0) {
-            if (p.tree) {
-                const uint32_t* w = p.tree + (int64_t)(rg.row0 + tok[i]) * p.tree_words;
-                int d = 0;
-                for (int x = 0; x < p.tree_words && 32 * x < rg.all; ++x) d += __builtin_popcount(w[x] & ~bits_from(rg.all - 32 * x));
-                low[i] = min(rg.context + d - p.window, rg.context);
-            } else {
-                low[i] = rg.context + tok[i] - p.window + 1;
             }
-        }
-    }
-    // (used here, so that the compiler's wait for q is not in the loop, where it would be one for the copies)
-    const uint32_t flip = p.scale_log2 < 0.0f ? 0x80008000u : 0u;
-#pragma unroll
-    for (int i = 0; i < RB; ++i)
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-            qf[i][s] = __builtin_bit_cast(x8, __builtin_bit_cast(u32x4_t, qf[i][s]) ^ flip);
-            asm volatile("" : "+v"(qf[i][s]));
-        }
-
-    f32x4_t o[RB][VE];
-    float mx[RB], sum[RB];  // the largest score, unscaled, and the sum of exponentials
-#pragma unroll
-    for (int i = 0; i < RB; ++i) {
-#pragma unroll
-        for (int m = 0; m < VE; ++m) o[i][m] = (f32x4_t){};
-        mx[i] = kNegInf;
-        sum[i] = 0.0f;
-    }
-
-    // Which of the keys 32 n .. of a tile row i of this lane sees.  (Lanes' numbers by way of a register that the compiler
-    // does not look through: what the rare tiles need is not to be kept over the others.)
-    auto row_sees = [&](int i, int n, const uint32_t* good, int key0) {
-        const int x0 = key0 + 32 * n - rg.context;  // the first key's number among the tokens
-        uint32_t bits;
-        if (!p.tree) {
-            bits = ~bits_from(tok[i] - x0 + 1);
-        } else {
-            const uint32_t* words = p.tree + (int64_t)(rg.row0 + tok[i]) * p.tree_words;
-            const int w = x0 >> 5, sh = x0 & 31;
-            const uint32_t w0 = w >= 0 && w < p.tree_words ? words[w] : 0u;
-            const uint32_t w1 = w >= -1 && w + 1 < p.tree_words ? words[w + 1] : 0u;
-            bits = __builtin_amdgcn_alignbit(w1, w0, sh) | ~bits_from(-x0);
-        }
-        return bits & good[n] & bits_from(low[i] - key0 - 32 * n);
-    };
-    // A tile that not every row sees whole: values that are not finite are added to the rows that see their keys
-    // (infinities and NaN: a probability, which is positive, would not change them), and become zeros.
-    auto set_apart = [&](int stage, const uint32_t* good, int key0) {
-        char* const vt = stages + stage * S::STAGE + KT * KB;
-        int own_lane = lane;
-        asm volatile("" : "+v"(own_lane));
-        bool strange = false;
-        for (int i = (wr * 64 + own_lane) * 16; i < KT * KB; i += WR * 1024) {
-            const u32x4_t v = *(const u32x4_t*)(vt + i);
-#pragma unroll
-            for (int y = 0; y < 4; ++y) strange = strange || not_finite<T, E4M3>(v[y]);
-        }
-        if constexpr (WR > 1) {  // (a part of the stage a wave, and all of them come by here)
-            strange_[stage][wr] = __any(strange);
-            barrier_lds();
-            const u32x4_t any = *(const u32x4_t*)strange_[stage];
-            strange = any[0] | any[1] | any[2] | any[3];
-        }
-        if (!__any(strange)) return;
-        if (rows > 0)
+            // (used here, so that the compiler's wait for q is not in the loop, where it would be one for the
+            // copies)
+            const uint32_t flip = p.scale_log2 < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
             for (int i = 0; i < RB; ++i)
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const uint32_t sees = row_sees(i, n, good, key0);
-                    for (int k = 0; k < 32; ++k) {
-                        const char* row = vt + (32 * n + k) * KB;
+                for (int s = 0; s < STEPS; ++s) {
+                    qf[i][s] = __builtin_bit_cast(x8, __builtin_bit_cast(u32x4_t, qf[i][s]) ^ flip);
+                    asm volatile("" : "+v"(qf[i][s]));
+                }
+
+            f32x4_t o[RB][VE];
+            float mx[RB], sum[RB];  // the largest score, unscaled, and the sum of exponentials
 #pragma unroll
-                        for (int m = 0; m < VE; ++m) {
-                            const int d = 16 * m + 4 * (own_lane >> 4);
-                            const char* at = row + ((d * ES / 16) ^ swz(k & 15)) * 16 + d * ES % 16;
-                            uint32_t u[2];
-                            if constexpr (E4M3) {
-                                const uint32_t w = *(const uint32_t*)at;
-                                u[0] = H::from_fp8(w, false);
-                                u[1] = H::from_fp8(w, true);
-                            } else {
-                                u[0] = *(const uint32_t*)at;
-                                u[1] = *(const uint32_t*)(at + 4);
-                            }
+            for (int i = 0; i < RB; ++i) {
 #pragma unroll
-                            for (int y = 0; y < 4; ++y) {
-                                const float z = (float)__builtin_bit_cast(T, (uint16_t)(u[y >> 1] >> 16 * (y & 1)));
-                                o[i][m][y] += (sees >> k & 1) && !(fabsf(z) < __builtin_inff()) ? z : 0.0f;
+                for (int m = 0; m < VE; ++m) o[i][m] = (f32x4_t){};
+                mx[i] = kNegInf;
+                sum[i] = 0.0f;
+            }
+
+            // Which of the keys 32 n .. of a tile row i of this lane sees.  (Lanes' numbers by way of a register
+            // that the compiler does not look through: what the rare tiles need is not to be kept over the others.)
+            auto row_sees = [&](int i, int n, const uint32_t* good, int key0) {
+                const int x0 = key0 + 32 * n - rg.context;  // the first key's number among the tokens
+                uint32_t bits;
+                if (!p.tree) {
+                    bits = ~bits_from(tok[i] - x0 + 1);
+                } else {
+                    const uint32_t* words = p.tree + (int64_t)(rg.row0 + tok[i]) * p.tree_words;
+                    const int w = x0 >> 5, sh = x0 & 31;
+                    const uint32_t w0 = w >= 0 && w < p.tree_words ? words[w] : 0u;
+                    const uint32_t w1 = w >= -1 && w + 1 < p.tree_words ? words[w + 1] : 0u;
+                    bits = __builtin_amdgcn_alignbit(w1, w0, sh) | ~bits_from(-x0);
+                }
+                return bits & good[n] & bits_from(low[i] - key0 - 32 * n);
+            };
+            // A tile that not every row sees whole: values that are not finite are added to the rows that see their
+            // keys (infinities and NaN: a probability, which is positive, would not change them), and become zeros.
+            auto set_apart = [&](int stage, const uint32_t* good, int key0) {
+                char* const vt = stages + stage * S::STAGE + KT * KB;
+                int own_lane = lane;
+                asm volatile("" : "+v"(own_lane));
+                bool strange = false;
+                for (int i = (wr * 64 + own_lane) * 16; i < KT * KB; i += WR * 1024) {
+                    const u32x4_t v = *(const u32x4_t*)(vt + i);
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) strange = strange || not_finite<T, E4M3>(v[y]);
+                }
+                if constexpr (WR > 1) {  // (a part of the stage a wave, and all of them come by here)
+                    strange_[stage][wr] = __any(strange);
+                    barrier_lds();
+                    const u32x4_t any = *(const u32x4_t*)strange_[stage];
+                    strange = any[0] | any[1] | any[2] | any[3];
+                }
+                if (!__any(strange)) return;
+                if (rows > 0)
+#pragma unroll
+                    for (int i = 0; i < RB; ++i)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            const uint32_t sees = row_sees(i, n, good, key0);
+                            for (int k = 0; k < 32; ++k) {
+                                const char* row = vt + (32 * n + k) * KB;
+#pragma unroll
+                                for (int m = 0; m < VE; ++m) {
+                                    const int d = 16 * m + 4 * (own_lane >> 4);
+                                    const char* at = row + ((d * ES / 16) ^ swz(k & 15)) * 16 + d * ES % 16;
+                                    uint32_t u[2];
+                                    if constexpr (E4M3) {
+                                        const uint32_t w = *(const uint32_t*)at;
+                                        u[0] = H::from_fp8(w, false);
+                                        u[1] = H::from_fp8(w, true);
+                                    } else {
+                                        u[0] = *(const uint32_t*)at;
+                                        u[1] = *(const uint32_t*)(at + 4);
+                                    }
+#pragma unroll
+                                    for (int y = 0; y < 4; ++y) {
+                                        const float z = (float)__builtin_bit_cast(T, (uint16_t)(u[y >> 1] >> 16 * (y & 1)));
+                                        o[i][m][y] += (sees >> k & 1) && !(fabsf(z) < __builtin_inff()) ? z : 0.0f;
+                                    }
+                                }
                             }
+                        }
+                if constexpr (WR > 1) barrier_lds();
+                else wave_lds_exchange();
+                for (int i = (wr * 64 + own_lane) * 4; i < KT * KB; i += WR * 256) {
+                    uint32_t v = *(const uint32_t*)(vt + i);
+                    if constexpr (E4M3) {
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) v = (v >> 8 * y & 0x7f) == 0x7f ? v & ~(0xffu << 8 * y) : v;
+                    } else {
+                        v = not_finite<T, E4M3>(v & 0xffffu) ? v & 0xffff0000u : v;
+                        v = not_finite<T, E4M3>(v & 0xffff0000u) ? v & 0xffffu : v;
+                    }
+                    *(uint32_t*)(vt + i) = v;
+                }
+                if constexpr (WR > 1) barrier_lds();
+                else wave_lds_exchange();
+            };
+            // The scores of a tile; SPREAD: with the copies of the next one among the products.
+            auto scores = [&](auto spread, const char* kt, f32x4_t (*s)[2 * NT]) {
+                constexpr int QS = E4M3 ? STEPS / 2 : STEPS, GROUPS = QS * 2 * NT, COPIES = 2 * NH * HALF;
+#pragma unroll
+                for (int i = 0; i < RB; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2 * NT; ++h) s[i][h] = (f32x4_t){};
+                i32x4_t kf[2][2 * NT];
+                auto read = [&](int st) {
+#pragma unroll
+                    for (int h = 0; h < 2 * NT; ++h)
+                        kf[st & 1][h] = *(const i32x4_t*)(kt + (16 * h + r16) * KB + ((4 * st + g4) ^ swz(r16)) * 16);
+                };
+                read(0);
+#pragma unroll
+                for (int st = 0; st < QS; ++st) {
+                    if (st + 1 < QS) read(st + 1);
+#pragma unroll
+                    for (int h = 0; h < 2 * NT; ++h) {
+                        const i32x4_t w = kf[st & 1][h];
+                        if constexpr (E4M3) {
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                u32x4_t u;
+                                u[0] = H::from_fp8(w[2 * y], false);
+                                u[1] = H::from_fp8(w[2 * y], true);
+                                u[2] = H::from_fp8(w[2 * y + 1], false);
+                                u[3] = H::from_fp8(w[2 * y + 1], true);
+#pragma unroll
+                                for (int i = 0; i < RB; ++i) s[i][h] = H::mma(__builtin_bit_cast(x8, u), qf[i][2 * st + y], s[i][h]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < RB; ++i) s[i][h] = H::mma(__builtin_bit_cast(x8, w), qf[i][st], s[i][h]);
+                        }
+                        if constexpr (decltype(spread)::value) {
+                            const int g = st * 2 * NT + h;
+#pragma unroll
+                            for (int i = 0; i < COPIES; ++i)
+                                if (i * GROUPS / COPIES == g) copy(copies, i);
                         }
                     }
                 }
-        if constexpr (WR > 1) barrier_lds();
-        else wave_lds_exchange();
-        for (int i = (wr * 64 + own_lane) * 4; i < KT * KB; i += WR * 256) {
-            uint32_t v = *(const uint32_t*)(vt + i);
-            if constexpr (E4M3) {
+            };
+            auto products = [&](int stage, bool plain, bool spread, const uint32_t* good, int key0) {
+                const char* const kt = stages + stage * S::STAGE;
+                const char* const vt = kt + KT * KB;
+                float x[RB][8 * NT];
+                f32x4_t s[RB][2 * NT];
+                if (spread) scores(std::true_type{}, kt, s);
+                else scores(std::false_type{}, kt, s);
 #pragma unroll
-                for (int y = 0; y < 4; ++y) v = (v >> 8 * y & 0x7f) == 0x7f ? v & ~(0xffu << 8 * y) : v;
-            } else {
-                v = not_finite<T, E4M3>(v & 0xffffu) ? v & 0xffff0000u : v;
-                v = not_finite<T, E4M3>(v & 0xffff0000u) ? v & 0xffffu : v;
-            }
-            *(uint32_t*)(vt + i) = v;
-        }
-        if constexpr (WR > 1) barrier_lds();
-        else wave_lds_exchange();
-    };
-    // The scores of a tile; SPREAD: with the copies of the next one among the products.
-    auto scores = [&](auto spread, const char* kt, f32x4_t (*s)[2 * NT]) {
-        constexpr int QS = E4M3 ? STEPS / 2 : STEPS, GROUPS = QS * 2 * NT, COPIES = 2 * NH * HALF;
+                for (int i = 0; i < RB; ++i)
 #pragma unroll
-        for (int i = 0; i < RB; ++i)
+                    for (int j = 0; j < 8 * NT; ++j) x[i][j] = s[i][j >> 2][j & 3];
+                if (!plain) {
+                    asm volatile("");  // (a branch: as selects it would run for every tile)
 #pragma unroll
-            for (int h = 0; h < 2 * NT; ++h) s[i][h] = (f32x4_t){};
-        i32x4_t kf[2][2 * NT];
-        auto read = [&](int st) {
+                    for (int i = 0; i < RB; ++i)
 #pragma unroll
-            for (int h = 0; h < 2 * NT; ++h)
-                kf[st & 1][h] = *(const i32x4_t*)(kt + (16 * h + r16) * KB + ((4 * st + g4) ^ swz(r16)) * 16);
-        };
-        read(0);
+                        for (int n = 0; n < NT; ++n) {
+                            const uint32_t sees = row_sees(i, n, good, key0) >> 4 * g4;
 #pragma unroll
-        for (int st = 0; st < QS; ++st) {
-            if (st + 1 < QS) read(st + 1);
+                            for (int j = 0; j < 8; ++j)
+                                x[i][8 * n + j] = sees >> ((j < 4 ? 0 : 16) + (j & 3)) & 1 ? x[i][8 * n + j] : kNegInf;
+                        }
+                }
+                // Values, 16 elements of 8 keys a lane, asked for before the softmax that their products wait for
+                constexpr int VG = RB > 1 || VE < 8 ? 4 : 8;  // products whose values are in registers at once
+                x8 v[VG];
+                auto read_values = [&](int n, int m0) {
 #pragma unroll
-            for (int h = 0; h < 2 * NT; ++h) {
-                const i32x4_t w = kf[st & 1][h];
-                if constexpr (E4M3) {
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        u32x4_t u;
-                        u[0] = H::from_fp8(w[2 * y], false);
-                        u[1] = H::from_fp8(w[2 * y], true);
-                        u[2] = H::from_fp8(w[2 * y + 1], false);
-                        u[3] = H::from_fp8(w[2 * y + 1], true);
-#pragma unroll
-                        for (int i = 0; i < RB; ++i) s[i][h] = H::mma(__builtin_bit_cast(x8, u), qf[i][2 * st + y], s[i][h]);
+                    for (int y = 0; y < VG; ++y) {
+                        const int m = m0 + y;
+                        if constexpr (E4M3) {
+                            // 8 rows of 16 bytes, row r from lanes 2 r and 2 r + 1
+                            const int r = r16 >> 1, key = (r < 4 ? 0 : 16) + 4 * g4 + (r & 3);
+                            const i32x2_t w = lds_read_tr8(vt + (32 * n + key) * KB + (m ^ swz(key & 15)) * 16 + 8 * (r16 & 1));
+                            v[y] = __builtin_bit_cast(x8, (u32x4_t){H::from_fp8(w[0], false), H::from_fp8(w[0], true),
+                                                                    H::from_fp8(w[1], false), H::from_fp8(w[1], true)});
+                        } else {
+                            // twice 4 rows of 16 elements, row r from lanes 4 r .. 4 r + 3
+                            const int key = 4 * g4 + (r16 >> 2), c = 2 * m + (r16 >> 1 & 1);
+                            const char* at = vt + (32 * n + key) * KB + (c ^ swz(key)) * 16 + 8 * (r16 & 1);
+                            union {
+                                s16x4_t half[2];
+                                x8 all;
+                            } u;
+                            u.half[0] = lds_read_tr16(at);
+                            u.half[1] = lds_read_tr16(at + 16 * KB);
+                            v[y] = u.all;
+                        }
                     }
-                } else {
+                };
+                read_values(0, 0);
+                float top[RB];
+                bool higher = false;
 #pragma unroll
-                    for (int i = 0; i < RB; ++i) s[i][h] = H::mma(__builtin_bit_cast(x8, w), qf[i][st], s[i][h]);
+                for (int i = 0; i < RB; ++i) {
+                    top[i] = x[i][0];
+#pragma unroll
+                    for (int j = 1; j < 8 * NT; ++j) top[i] = fmaxf(top[i], x[i][j]);
+                    top[i] = max_over_groups(top[i]);
+                    higher = higher || top[i] > mx[i];
                 }
-                if constexpr (decltype(spread)::value) {
-                    const int g = st * 2 * NT + h;
+                if (__any(higher)) {
 #pragma unroll
-                    for (int i = 0; i < COPIES; ++i)
-                        if (i * GROUPS / COPIES == g) copy(copies, i);
+                    for (int i = 0; i < RB; ++i) {
+                        const float m2 = fmaxf(mx[i], top[i]);
+                        // (o may hold infinities: from the least factor on they stay)
+                        const float f = mx[i] == kNegInf ? 1.0f : fmaxf(__builtin_amdgcn_exp2f((mx[i] - m2) * scale), 0x1p-126f);
+                        mx[i] = m2;
+                        sum[i] *= f;
+#pragma unroll
+                        for (int m = 0; m < VE; ++m)
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) o[i][m][y] *= f;
+                    }
                 }
-            }
-        }
-    };
-    auto products = [&](int stage, bool plain, bool spread, const uint32_t* good, int key0) {
-        const char* const kt = stages + stage * S::STAGE;
-        const char* const vt = kt + KT * KB;
-        float x[RB][8 * NT];
-        f32x4_t s[RB][2 * NT];
-        if (spread) scores(std::true_type{}, kt, s);
-        else scores(std::false_type{}, kt, s);
-#pragma unroll
-        for (int i = 0; i < RB; ++i)
-#pragma unroll
-            for (int j = 0; j < 8 * NT; ++j) x[i][j] = s[i][j >> 2][j & 3];
-        if (!plain) {
-            asm volatile("");  // (a branch: as selects it would run for every tile)
-#pragma unroll
-            for (int i = 0; i < RB; ++i)
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    const uint32_t sees = row_sees(i, n, good, key0) >> 4 * g4;
+                    if (n > 0) read_values(n, 0);
+                    x8 upper[RB], lower[RB];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) x[i][8 * n + j] = sees >> ((j < 4 ? 0 : 16) + (j & 3)) & 1 ? x[i][8 * n + j] : kNegInf;
+                    for (int i = 0; i < RB; ++i) {
+                        const float m0 = mx[i] == kNegInf ? 0.0f : mx[i] * scale;
+                        u32x4_t pu, pl;
+#pragma unroll
+                        for (int j = 0; j < 8; j += 2) {
+                            float& e0 = x[i][8 * n + j];
+                            float& e1 = x[i][8 * n + j + 1];
+                            e0 = __builtin_amdgcn_exp2f(fmaf(e0, scale, -m0));
+                            e1 = __builtin_amdgcn_exp2f(fmaf(e1, scale, -m0));
+                            sum[i] += e0;
+                            sum[i] += e1;
+                            uint32_t u, l;
+                            H::parts(e0, e1, u, l);
+                            pu[j / 2] = u;
+                            pl[j / 2] = l;
+                        }
+                        upper[i] = __builtin_bit_cast(x8, pu);
+                        lower[i] = __builtin_bit_cast(x8, pl);
+                    }
+#pragma unroll
+                    for (int m0 = 0; m0 < VE; m0 += VG) {
+                        if (m0 > 0) read_values(n, m0);
+#pragma unroll
+                        for (int y = 0; y < VG; ++y)
+#pragma unroll
+                            for (int i = 0; i < RB; ++i) o[i][m0 + y] = H::mma(v[y], upper[i], o[i][m0 + y]);
+#pragma unroll
+                        for (int y = 0; y < VG; ++y)
+#pragma unroll
+                            for (int i = 0; i < RB; ++i) o[i][m0 + y] = H::mma(v[y], lower[i], o[i][m0 + y]);
+                    }
                 }
-        }
-        // Values, 16 elements of 8 keys a lane, asked for before the softmax that their products wait for
-        constexpr int VG = RB > 1 || VE < 8 ? 4 : 8;  // products whose values are in registers at once
-        x8 v[VG];
-        auto read_values = [&](int n, int m0) {
+            };
+
+            auto compute = [&](int stage, uint32_t* good, int key0, bool spread) {
+                if constexpr (ALIGNED && WR > 1) {
+                    const u32x4_t is = *(const u32x4_t*)there_[stage];
+                    good[0] &= __builtin_amdgcn_readfirstlane(is[0] | is[1]);
+                    good[1] &= __builtin_amdgcn_readfirstlane(is[2] | is[3]);
+                }
+                bool plain = key0 >= rg.sure && key0 + KT <= rg.safe;
 #pragma unroll
-            for (int y = 0; y < VG; ++y) {
-                const int m = m0 + y;
-                if constexpr (E4M3) {
-                    // 8 rows of 16 bytes, row r from lanes 2 r and 2 r + 1
-                    const int r = r16 >> 1, key = (r < 4 ? 0 : 16) + 4 * g4 + (r & 3);
-                    const i32x2_t w = lds_read_tr8(vt + (32 * n + key) * KB + (m ^ swz(key & 15)) * 16 + 8 * (r16 & 1));
-                    v[y] = __builtin_bit_cast(x8, (u32x4_t){H::from_fp8(w[0], false), H::from_fp8(w[0], true),
-                                                            H::from_fp8(w[1], false), H::from_fp8(w[1], true)});
+                for (int n = 0; n < NT; ++n) plain = plain && good[n] == ~0u;
+                if (!plain) set_apart(stage, good, key0);
+                if (rows > 0) products(stage, plain, spread, good, key0);
+            };
+            for (int r = 0; r < tiles; ++r) {
+                uint32_t good[NT];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) good[n] = tile.good[n];
+                settle(r & 1);
+                if constexpr (ALIGNED) wait_vmcnt<0>();
+                if constexpr (WR > 1) barrier_lds();
+                else wave_lds_exchange();
+                bool spread = false;
+                if (r + 1 < tiles) {
+                    spread = !issue(next, (r + 1) & 1, rows > 0, copies);
+                    tile = next;
+                    next = look(first + (r + 2) * ROUND);
+                }
+                compute(r & 1, good, first + r * ROUND, spread);
+                wave_lds_exchange();
+            }
+
+            // ---- sums, and the groups' parts ----------------------------------------------------
+#pragma unroll
+            for (int i = 0; i < RB; ++i) {
+                sum[i] += __shfl_xor(sum[i], 16);
+                sum[i] += __shfl_xor(sum[i], 32);
+                // a NaN among the scores passed by the maximum: as an infinite one it makes
+                // every later factor of this part NaN and of the others 0
+                mx[i] = sum[i] != sum[i] ? -kNegInf : mx[i] * scale;
+            }
+            // 4 elements from d on of a row with maximum m and sum l
+            auto store = [&](int row, int d, f32x4_t a, float m, float l) {
+                if (part) {
+                    const int64_t at = slot * S::ROWS + row - blk * S::ROWS;
+                    *(f32x4_t*)(p.po + at * p.D + d) = a;
+                    if (d == 0) {
+                        p.pml[2 * at] = m;
+                        p.pml[2 * at + 1] = l;
+                    }
                 } else {
-                    // twice 4 rows of 16 elements, row r from lanes 4 r .. 4 r + 3
-                    const int key = 4 * g4 + (r16 >> 2), c = 2 * m + (r16 >> 1 & 1);
-                    const char* at = vt + (32 * n + key) * KB + (c ^ swz(key)) * 16 + 8 * (r16 & 1);
-                    union {
-                        s16x4_t half[2];
-                        x8 all;
-                    } u;
-                    u.half[0] = lds_read_tr16(at);
-                    u.half[1] = lds_read_tr16(at + 16 * KB);
-                    v[y] = u.all;
+                    const int t = row / p.G, h = hk * p.G + row - t * p.G;
+                    const float n = m == kNegInf ? 0.0f : p.v_scale / l;
+                    T* out = (T*)p.out.p + (int64_t)(rg.row0 + t) * p.out.ts + (int64_t)h * p.out.hs + d;
+                    store4<T>(out, a[0] * n, a[1] * n, a[2] * n, a[3] * n);
+                    if (d == 0 && p.lse)
+                        p.lse[(int64_t)(rg.row0 + t) * p.Hq + h] = m == kNegInf ? kNegInf : 0.6931471805599453f * m + logf(l);
+                }
+            };
+            if constexpr (WK == 1) {
+                // lane l holds elements 16 m + 4 g .. + 3 of row l % 16
+                constexpr float down = 1.0f / H::kLift;
+#pragma unroll
+                for (int i = 0; i < RB; ++i)
+                    if (16 * i + r16 < rows)
+#pragma unroll
+                        for (int m = 0; m < VE; ++m) {
+                            const int d = 16 * m + 4 * g4;
+                            if (d < p.D)
+                                store(row0 + 16 * i + r16, d, o[i][m] * down, mx[i], sum[i]);
+                        }
+            } else {
+                float (*const lo_)[16][DP + 4] = (float (*)[16][DP + 4])lds;
+                auto top = [&](int i, int q) {
+                    float t = lm_[i][0][q];
+#pragma unroll
+                    for (int w = 1; w < WK; ++w) t = fmaxf(t, lm_[i][w][q]);
+                    return t;
+                };
+#pragma unroll
+                for (int i = 0; i < RB; ++i)
+                    if (g4 == 0) {
+                        lm_[i][wk][r16] = mx[i];
+                        ll_[i][wk][r16] = sum[i];
+                    }
+#pragma unroll
+                for (int i = 0; i < RB; ++i) {
+                    __syncthreads();  // (the rings end here; the last 16 rows' results are read)
+                    const float f = mx[i] == kNegInf ? 0.0f : 1.0f / H::kLift * __builtin_amdgcn_exp2f(mx[i] - top(i, r16));
+#pragma unroll
+                    for (int m = 0; m < VE; ++m) {
+                        f32x4_t v = {o[i][m][0] * f, o[i][m][1] * f, o[i][m][2] * f, o[i][m][3] * f};
+                        if (mx[i] == kNegInf) v = (f32x4_t){};
+                        *(f32x4_t*)&lo_[wk][r16][16 * m + 4 * g4] = v;
+                    }
+                    __syncthreads();
+                    for (int z = threadIdx.x; z < 16 * (DP / 4); z += WK * 64) {
+                        const int q = z / (DP / 4), d = z % (DP / 4) * 4;
+                        if (16 * i + q >= rows || d >= p.D) continue;
+                        const float tq = top(i, q);
+                        f32x4_t a = {};
+                        float l = 0.0f;
+#pragma unroll
+                        for (int w = 0; w < WK; ++w) {
+                            a += *(f32x4_t*)&lo_[w][q][d];
+                            const float mw = lm_[i][w][q];
+                            l += mw == kNegInf ? 0.0f : ll_[i][w][q] * __builtin_amdgcn_exp2f(mw - tq);
+                        }
+                        store(row0 + 16 * i + q, d, a, tq, l);
+                    }
                 }
             }
-        };
-        read_values(0, 0);
-        float top[RB];
-        bool higher = false;
-#pragma unroll
-        for (int i = 0; i < RB; ++i) {
-            top[i] = x[i][0];
-#pragma unroll
-            for (int j = 1; j < 8 * NT; ++j) top[i] = fmaxf(top[i], x[i][j]);
-            top[i] = max_over_groups(top[i]);
-            higher = higher || top[i] > mx[i];
         }
-        if (__any(higher)) {
-#pragma unroll
-            for (int i = 0; i < RB; ++i) {
-                const float m2 = fmaxf(mx[i], top[i]);
-                // (o may hold infinities: from the least factor on they stay)
-                const float f = mx[i] == kNegInf ? 1.0f : fmaxf(__builtin_amdgcn_exp2f((mx[i] - m2) * scale), 0x1p-126f);
-                mx[i] = m2;
-                sum[i] *= f;
-#pragma unroll
-                for (int m = 0; m < VE; ++m)
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) o[i][m][y] *= f;
-            }
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            if (n > 0) read_values(n, 0);
-            x8 upper[RB], lower[RB];
-#pragma unroll
-            for (int i = 0; i < RB; ++i) {
-                const float m0 = mx[i] == kNegInf ? 0.0f : mx[i] * scale;
-                u32x4_t pu, pl;
-#pragma unroll
-                for (int j = 0; j < 8; j += 2) {
-                    float& e0 = x[i][8 * n + j];
-                    float& e1 = x[i][8 * n + j + 1];
-                    e0 = __builtin_amdgcn_exp2f(fmaf(e0, scale, -m0));
-                    e1 = __builtin_amdgcn_exp2f(fmaf(e1, scale, -m0));
-                    sum[i] += e0;
-                    sum[i] += e1;
-                    uint32_t u, l;
-                    H::parts(e0, e1, u, l);
-                    pu[j / 2] = u;
-                    pl[j / 2] = l;
-                }
-                upper[i] = __builtin_bit_cast(x8, pu);
-                lower[i] = __builtin_bit_cast(x8, pl);
-            }
-#pragma unroll
-            for (int m0 = 0; m0 < VE; m0 += VG) {
-                if (m0 > 0) read_values(n, m0);
-#pragma unroll
-                for (int y = 0; y < VG; ++y)
-#pragma unroll
-                    for (int i = 0; i < RB; ++i) o[i][m0 + y] = H::mma(v[y], upper[i], o[i][m0 + y]);
-#pragma unroll
-                for (int y = 0; y < VG; ++y)
-#pragma unroll
-                    for (int i = 0; i < RB; ++i) o[i][m0 + y] = H::mma(v[y], lower[i], o[i][m0 + y]);
-            }
-        }
-    };
-
-    auto compute = [&](int stage, uint32_t* good, int key0, bool spread) {
-        if constexpr (ALIGNED && WR > 1) {
-            const u32x4_t is = *(const u32x4_t*)there_[stage];
-            good[0] &= __builtin_amdgcn_readfirstlane(is[0] | is[1]);
-            good[1] &= __builtin_amdgcn_readfirstlane(is[2] | is[3]);
-        }
-        bool plain = key0 >= rg.sure && key0 + KT <= rg.safe;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) plain = plain && good[n] == ~0u;
-        if (!plain) set_apart(stage, good, key0);
-        if (rows > 0) products(stage, plain, spread, good, key0);
-    };
-    for (int r = 0; r < tiles; ++r) {
-        uint32_t good[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) good[n] = tile.good[n];
-        settle(r & 1);
-        if constexpr (ALIGNED) wait_vmcnt<0>();
-        if constexpr (WR > 1) barrier_lds();
-        else wave_lds_exchange();
-        bool spread = false;
-        if (r + 1 < tiles) {
-            spread = !issue(next, (r + 1) & 1, rows > 0, copies);
-            tile = next;
-            next = look(first + (r + 2) * ROUND);
-        }
-        compute(r & 1, good, first + r * ROUND, spread);
-        wave_lds_exchange();
-    }
-
-    // ---- sums, and the groups' parts ----------------------------------------------------
-#pragma unroll
-    for (int i = 0; i < RB; ++i) {
-        sum[i] += __shfl_xor(sum[i], 16);
-        sum[i] += __shfl_xor(sum[i], 32);
-        // a NaN among the scores passed by the maximum: as an infinite one it makes
-        // every later factor of this part NaN and of the others 0
-        mx[i] = sum[i] != sum[i] ? -kNegInf : mx[i] * scale;
-    }
-    // 4 elements from d on of a row with maximum m and sum l
-    auto store = [&](int row, int d, f32x4_t a, float m, float l) {
-        if (part) {
-            const int64_t at = slot * S::ROWS + row - blk * S::ROWS;
-            *(f32x4_t*)(p.po + at * p.D + d) = a;
-            if (d == 0) {
-                p.pml[2 * at] = m;
-                p.pml[2 * at + 1] = l;
-            }
-        } else {
-            const int t = row / p.G, h = hk * p.G + row - t * p.G;
-            const float n = m == kNegInf ? 0.0f : p.v_scale / l;
-            T* out = (T*)p.out.p + (int64_t)(rg.row0 + t) * p.out.ts + (int64_t)h * p.out.hs + d;
-            store4<T>(out, a[0] * n, a[1] * n, a[2] * n, a[3] * n);
-            if (d == 0 && p.lse) p.lse[(int64_t)(rg.row0 + t) * p.Hq + h] = m == kNegInf ? kNegInf : 0.6931471805599453f * m + logf(l);
-        }
-    };
-    if constexpr (WK == 1) {
-        // lane l holds elements 16 m + 4 g .. + 3 of row l % 16
-        constexpr float down = 1.0f / H::kLift;
-#pragma unroll
-        for (int i = 0; i < RB; ++i)
-            if (16 * i + r16 < rows)
-#pragma unroll
-                for (int m = 0; m < VE; ++m) {
-                    const int d = 16 * m + 4 * g4;
-                    if (d < p.D)
-                        store(row0 + 16 * i + r16, d, (f32x4_t){o[i][m][0] * down, o[i][m][1] * down, o[i][m][2] * down, o[i][m][3] * down},
-                              mx[i], sum[i]);
-                }
-    } else {
-        float (*const lo_)[16][DP + 4] = (float (*)[16][DP + 4])lds;
-        auto top = [&](int i, int q) {
-            float t = lm_[i][0][q];
-#pragma unroll
-            for (int w = 1; w < WK; ++w) t = fmaxf(t, lm_[i][w][q]);
-            return t;
-        };
-#pragma unroll
-        for (int i = 0; i < RB; ++i)
-            if (g4 == 0) {
-                lm_[i][wk][r16] = mx[i];
-                ll_[i][wk][r16] = sum[i];
-            }
-#pragma unroll
-        for (int i = 0; i < RB; ++i) {
-            __syncthreads();  // (the rings end here; the last 16 rows' results are read)
-            const float f = mx[i] == kNegInf ? 0.0f : 1.0f / H::kLift * __builtin_amdgcn_exp2f(mx[i] - top(i, r16));
-#pragma unroll
-            for (int m = 0; m < VE; ++m) {
-                f32x4_t v = {o[i][m][0] * f, o[i][m][1] * f, o[i][m][2] * f, o[i][m][3] * f};
-                if (mx[i] == kNegInf) v = (f32x4_t){};
-                *(f32x4_t*)&lo_[wk][r16][16 * m + 4 * g4] = v;
-            }
-            __syncthreads();
-            for (int z = threadIdx.x; z < 16 * (DP / 4); z += WK * 64) {
-                const int q = z / (DP / 4), d = z % (DP / 4) * 4;
-                if (16 * i + q >= rows || d >= p.D) continue;
-                const float tq = top(i, q);
-                f32x4_t a = {};
-                float l = 0.0f;
-#pragma unroll
-                for (int w = 0; w < WK; ++w) {
-                    a += *(f32x4_t*)&lo_[w][q][d];
-                    const float mw = lm_[i][w][q];
-                    l += mw == kNegInf ? 0.0f : ll_[i][w][q] * __builtin_amdgcn_exp2f(mw - tq);
-                }
-                store(row0 + 16 * i + q, d, a, tq, l);
-            }
-        }
-    }
-
-    }
-    step = past;
-    if (step >= stop) return;
-    if (step >= place.before + place.cost) place = tree_place(p, ROUND, step, lanes);
-    __syncthreads();  // (the stages, and what met in LDS, are free)
+        step = past;
+        if (step >= stop) return;
+        if (step >= place.before + place.cost) place = tree_place(p, ROUND, step, lanes);
+        __syncthreads();  // (the stages, and what met in LDS, are free)
     }
 }
 
-// Joins the parts of the blocks of rows that lie in more than one stretch, DL lanes a row; with many parts all lanes
-// take one row after the other.
+// Joins the parts of the blocks of rows that lie in more than one stretch, DL lanes a row; with many parts all
+// lanes take one row after the other.
 template <class T, int DL>
 __global__ __launch_bounds__(256) void tree_join_kernel(TreeArgs p) {
     constexpr int RG = 256 / DL, FEW = 16;
