@@ -843,10 +843,11 @@ void tree_kernel(TreeArgs p) {
 }
 
 // Joins the parts of the blocks of rows that lie in more than one stretch, DL lanes a row; with many parts all
-// lanes take one row after the other.
+// lanes take one row after the other.  (Few parts are loaded without conditions, all at once: a load under one for
+// each part made 14.2 us of 13.2.)
 template <class T, int DL>
 __global__ __launch_bounds__(256) void tree_join_kernel(TreeArgs p) {
-    constexpr int RG = 256 / DL, FEW = 16;
+    constexpr int RG = 256 / DL;
     __shared__ float wt[kTreeGroups];
     __shared__ float red[2][4];
     __shared__ __attribute__((aligned(16))) float join[RG][DL * 4];
@@ -866,29 +867,34 @@ __global__ __launch_bounds__(256) void tree_join_kernel(TreeArgs p) {
         if (d == 0 && p.lse)
             p.lse[(int64_t)(rg.row0 + t) * p.Hq + h] = top == kNegInf ? kNegInf : 0.6931471805599453f * top + logf(l);
     };
-    if (n <= FEW) {
+    // N parts at most, all of whose loads are under way together (past the last: the last one's again)
+    auto few = [&](auto most) {
+        constexpr int N = decltype(most)::value;
         const int r = blockIdx.y * RG + g;
         if (r >= rows || d >= p.D) return;
-        float m[FEW], l[FEW], top = kNegInf, sum = 0.0f;
-        f32x4_t v[FEW], a = {};
+        float m[N], l[N], top = kNegInf, sum = 0.0f;
+        f32x4_t v[N], a = {};
 #pragma unroll
-        for (int i = 0; i < FEW; ++i) {
+        for (int i = 0; i < N; ++i) {
             const int64_t at = place_of(min(i, n - 1), r);
-            m[i] = i < n ? p.pml[2 * at] : kNegInf;
-            l[i] = i < n ? p.pml[2 * at + 1] : 0.0f;
-            v[i] = i < n ? *(const f32x4_t*)(p.po + at * p.D + d) : (f32x4_t){};
-            top = fmaxf(top, m[i]);
+            m[i] = p.pml[2 * at];
+            l[i] = p.pml[2 * at + 1];
+            v[i] = *(const f32x4_t*)(p.po + at * p.D + d);
         }
 #pragma unroll
-        for (int i = 0; i < FEW; ++i) {
+        for (int i = 0; i < N; ++i) top = fmaxf(top, m[i]);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
             if (i >= n || m[i] == kNegInf) continue;
             const float f = __builtin_amdgcn_exp2f(m[i] - top);
             sum += f * l[i];
             a += f * v[i];
         }
         store(r, a, top, sum);
-        return;
-    }
+    };
+    if (n <= 2) return few(std::integral_constant<int, 2>{});
+    if (n <= 4) return few(std::integral_constant<int, 4>{});
+    if (n <= 16) return few(std::integral_constant<int, 16>{});
     for (int r = blockIdx.y; r < rows; r += gridDim.y) {
         float top = kNegInf, l = 0.0f;
         for (int i = c; i < n; i += 256) top = fmaxf(top, p.pml[2 * place_of(i, r)]);
@@ -929,10 +935,13 @@ hipError_t run_shape(const TreeArgs& a, hipStream_t st) {
     hipLaunchKernelGGL((tree_kernel<T, DP, E4M3, ALIGNED, WR, RB>), dim3(a.groups), dim3(S::WAVES * 64), 0, st, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.po) return e;
-    // (few parts: 256 / (DP / 4) rows a workgroup; many: rows y, y + the grid's, .. one by one)
-    constexpr int RG = 256 / (DP / 4);
-    const int rows = min(S::ROWS, a.max_nodes * a.G), least = (S::ROWS + RG - 1) / RG;
-    hipLaunchKernelGGL((tree_join_kernel<T, DP / 4>), dim3(a.groups - 1, min(rows, max(least, 32))), dim3(256), 0, st, a);
+    // Few parts: 256 / (DP / 4) rows a workgroup; many: rows y, y + the grid's, .. one by one.  (32 for blocks of 128
+    // rows, half of which go at once where parts are few, took 13.2 us for 512 parts, 16 take 11.9; for blocks of 64
+    // rows and 32 parts 16 take 8.4, 32 7.5.)
+    constexpr int RG = 256 / (DP / 4), MOST = S::ROWS > 64 ? 16 : 32;
+    static_assert(MOST * RG >= S::ROWS, "all rows of a block");
+    hipLaunchKernelGGL((tree_join_kernel<T, DP / 4>), dim3(a.groups - 1, min(min(S::ROWS, a.max_nodes * a.G), MOST)), dim3(256),
+                       0, st, a);
     return hipGetLastError();
 }
 template <class T, int DP, bool E4M3, bool ALIGNED>
