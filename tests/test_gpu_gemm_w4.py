@@ -160,3 +160,19 @@ def test_large_offsets():
 def test_many_columns(M, N, K, group, elem, dt):
     c = make(M, N, K, group, elem=elem, dt=dt, seed=M)
     check(tcm.gemm_w4(*c, elem=elem), *c, elem)
+
+
+@pytest.mark.parametrize("group,elem", [(32, "u4"), (64, "u4"), (128, "u4"), (32, "e2m1")])
+def test_scales_at_any_address(group, elem):
+    """Scales and zeros that begin at any element, which decides how many of them a lane loads at once."""
+    for M in (3, 20):
+        x, w, s, z = make(M, 70, 1024, group, elem=elem, dt=HF, seed=group)
+        def moved(t, by):
+            room = torch.zeros(t.numel() + 16, dtype=t.dtype, device=DEV)
+            at = room[by:by + t.numel()].view(t.shape)
+            at.copy_(t)
+            return at
+
+        for a, b in ((1, 0), (0, 1), (2, 2), (3, 1), (4, 2), (8, 4)):
+            got = tcm.gemm_w4(x, w, moved(s, a), None if z is None else moved(z, b), elem=elem, out_dtype=F32)
+            check(got, x, w, s, z, elem)
