@@ -31,7 +31,7 @@ import tensor_core_matrix_amd as tcm  # noqa: E402
 class Layer:
     """Weights and a paged cache of one layer."""
 
-    def __init__(self, width=1024, heads=16, kv_heads=4, head_dim=64, hidden=1536, group=64, pages=256, page_size=16,
+    def __init__(self, width=1024, heads=16, kv_heads=4, head_dim=64, hidden=1280, group=64, pages=256, page_size=16,
                  dtype=torch.bfloat16, device="cuda", seed=0):
         g = torch.Generator().manual_seed(seed)
         n = lambda *s, sd=1.0: (torch.randn(s, generator=g) * sd).to(dtype).to(device)  # noqa: E731
