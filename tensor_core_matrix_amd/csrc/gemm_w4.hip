@@ -6,7 +6,7 @@
 //
 //   M   N      K     elements, group, type      us     weights and scales, TB/s
 //   1   4096   4096  U4, 128, zeros, bf16       8.3    1.1  (most of it the call itself)
-//   12  12288  4096  E2M1, 32, bf16             14.8   1.8
+//   12  12288  4096  E2M1, 32, bf16             10.9   2.5
 //   48  32003  4096  U4, 64, fp16 to fp32       28.5   2.4
 //
 // A wave takes 16 columns (rows of W) and blocks of 128 values of K: a lane reads 16 bytes, 32 values of one
@@ -392,15 +392,18 @@ bool share(W4Args& a, int rows, int cus) {
         a.kc = 512;
         return false;
     }
-    // Waves side by side, as few as leave a workgroup for every compute unit; the others share K.  A stage of X
-    // is a batch of each of those, or all of K where it fits.
+    // Waves side by side; the others share K.  As few as give no more workgroups than run at once: two on a compute
+    // unit, or one where X takes more than half of its LDS (12 rows, 12288 x 4096: 384 workgroups of 96 KB took 15.7 us
+    // in two rounds, 192 take 11.8).  A stage of X is a batch of each of the waves that share K, or all of K where it
+    // fits.
     constexpr int waves = waves_of(1), batch = 128 * depth_of(1);
     for (a.wn = 1;; a.wn *= 2) {
         const int kc = batch * (waves / a.wn), all = a.K > 0 ? (a.K + kc - 1) / kc * kc : kc;
         const bool whole = (int64_t)rows * all * 2 <= 2 * kStageBytes;
         a.kc = whole ? all : kc;
         const bool fits = whole || rows * kc * 2 <= kStageBytes;
-        if (a.wn == waves || (fits && (a.N + 16 * a.wn - 1) / (16 * a.wn) <= 2 * cus)) return whole;
+        const int at_once = rows * a.kc * 2 * (whole ? 1 : 2) <= 80 * 1024 ? 2 * cus : cus;
+        if (a.wn == waves || (fits && (a.N + 16 * a.wn - 1) / (16 * a.wn) <= at_once)) return whole;
     }
 }
 
