@@ -80,12 +80,15 @@ __device__ __forceinline__ float row_sum(float x, float* red) {
     return x;
 }
 
-// 1 / sqrt(x): the hardware's approximation (1 ulp) and one Newton step
+// 1 / sqrt(x): the hardware's approximation (1 ulp) and one Newton step.  The instruction takes subnormal numbers for
+// zero, so those go through it 2^24 times as large.
 __device__ __forceinline__ float inv_sqrt(float x) {
-    const float r = __builtin_amdgcn_rsqf(x);
-    const float e = 0.5f - 0.5f * x * r * r;
+    const bool small = x < 0x1p-126f;
+    const float y = small ? x * 0x1p24f : x;
+    const float r = __builtin_amdgcn_rsqf(y);
+    const float e = 0.5f - 0.5f * y * r * r;
     // (zero, infinite and NaN x have no step)
-    return e == e ? fmaf(r, e, r) : r;
+    return (e == e ? fmaf(r, e, r) : r) * (small ? 0x1p12f : 1.0f);
 }
 
 // The 8 elements of this lane, of 32 that four lanes share, in E4M3, and their scale
