@@ -103,12 +103,15 @@ __device__ __forceinline__ float head_sum(float x) {
     return x;
 }
 
-// 1 / sqrt(x): the hardware's approximation (1 ulp) and one Newton step
+// 1 / sqrt(x): the hardware's approximation (1 ulp) and one Newton step.  The instruction takes subnormal numbers for
+// zero, so those go through it 2^24 times as large.
 __device__ __forceinline__ float inv_sqrt(float x) {
-    const float r = __builtin_amdgcn_rsqf(x);
-    const float e = 0.5f - 0.5f * x * r * r;
+    const bool small = x < 0x1p-126f;
+    const float y = small ? x * 0x1p24f : x;
+    const float r = __builtin_amdgcn_rsqf(y);
+    const float e = 0.5f - 0.5f * y * r * r;
     // (zero, infinite and NaN x have no step)
-    return e == e ? r + r * e : r;
+    return (e == e ? r + r * e : r) * (small ? 0x1p12f : 1.0f);
 }
 
 // The unit u of a head: where its elements are, and the first of its pairs.
@@ -399,7 +402,8 @@ __global__ __launch_bounds__(256) void norm_rope_bwd_kernel(RopeArgs p) {
                 ss = head_sum<L>(ss);
                 gx = head_sum<L>(gx);
                 const float r = inv_sqrt(ss * p.inv_d + p.eps);
-                const float m = r * r * gx * p.inv_d;  // mean(g h) r
+                // mean(g h) r (past 2^64 the square of r is past fp32)
+                const float m = (r < 0x1p63f ? r * r * gx : r * gx * r) * p.inv_d;
 #pragma unroll
                 for (int n = 0; n < NU; ++n)
 #pragma unroll
