@@ -85,10 +85,11 @@ def _weight(w, D, dtype, dev):
     return _expect(w, "weight", (D,), w.dtype, dev), _OUT[w.dtype]
 
 
-def _summed(x, residual, sum_out, shape, dev):
-    """(x, residual, sum) as (address, stride) pairs, and the sum's tensor."""
+def _summed(x, residual, sum_out, shape, dev, out=None):
+    """(x, residual, sum) as (address, stride) pairs, and the sum's tensor: x itself where nothing is added to it
+    and out does not overwrite it."""
     dt = (x.dtype,)
-    if sum_out is None and residual is not None:
+    if sum_out is None and (residual is not None or (out is not None and out.data_ptr() == x.data_ptr())):
         sum_out = torch.empty(shape, dtype=x.dtype, device=x.device)
     none = (None, 0)
     return (_rows(x, "x", shape, dt, dev), none if residual is None else _rows(residual, "residual", shape, dt, dev),
@@ -99,13 +100,14 @@ def _summed(x, residual, sum_out, shape, dev):
 def add_rms_norm(x, weight=None, residual=None, eps=1e-6, out=None, out_dtype=None, sum_out=None):
     """(out, s): s = x + residual (x without one) rounded to x's type, and out = weight s / sqrt(mean(s^2) +
     eps) for every row, of s before it is rounded.  x, residual, s (T, D) float16/bfloat16 with contiguous rows; weight
-    (D,) of x's type or float32; out of x's type or float32.  sum_out and out may be x or residual."""
+    (D,) of x's type or float32; out of x's type or float32.  sum_out and out may be x or residual; without a residual
+    and sum_out s is x itself, or a copy of it where out is x."""
     code = _half(x, "x")
     dev = x.get_device()
     T, D = shape = x.shape
     if out is None:
         out = torch.empty(shape, dtype=out_dtype or x.dtype, device=x.device)
-    (xp, ldx), (rp, ldr), (sp, lds), s = _summed(x, residual, sum_out, shape, dev)
+    (xp, ldx), (rp, ldr), (sp, lds), s = _summed(x, residual, sum_out, shape, dev, out)
     op, ldo = _rows(out, "out", shape, (x.dtype, torch.float32), dev)
     wp, wt = _weight(weight, D, x.dtype, dev)
     _run(dev, lib().tcm_add_rms_norm, xp, ldx, rp, ldr, wp, wt, eps, sp, lds, op, ldo, T, D, code, _OUT[out.dtype])
