@@ -342,7 +342,9 @@ tcm_status tcm_paged_tree_attention(const tcm_heads* q, const tcm_cache* cache,
     a.page_shift = 31 + s2;
     a.max_len = (int32_t)max_len;
     a.max_nodes = (int32_t)max_nodes;
-    a.window = window > max_len ? 0 : (int32_t)window;
+    // A window that keeps no row from any key is none.  (A sequence may have more tokens than keys, so a chain's last
+    // ones may be max_len + max_nodes places, at most 2^31, behind a key.)
+    a.window = window >= max_len + max_nodes ? 0 : (int32_t)window;
     a.groups = (int32_t)groups;
     a.rows = (int32_t)rows;
     a.scale_log2 = scale * (e4m3 ? cache->k_scale : 1.0f) * 1.4426950408889634f;

@@ -471,6 +471,7 @@ void tree_kernel(TreeArgs p) {
                     } else {
                         low[i] = rg.context + tok[i] - p.window + 1;
                     }
+                    low[i] = max(low[i], 0);
                 }
             }
             // (used here, so that the compiler's wait for q is not in the loop, where it would be one for the
