@@ -237,6 +237,8 @@ def paged_tree_attention(q, k_cache, v_cache, block_table, lengths, starts, max_
         if tree.dim() != 2:
             raise ValueError(f"tree must be ({T}, words) int64")
         words = tree.shape[1]
+        if 64 * words < max_nodes:  # (none at all would have no address, and be a chain)
+            raise ValueError(f"tree must have a bit for each of {max_nodes} tokens, not {words} words")
         tree = _expect(tree, "tree", (T, words), torch.int64, dev)
     cache = _cache(k_cache, v_cache, k_scale, v_scale, Hk, D, dt, dev)
     ws, nbytes, keep = _workspace(workspace, dev, paged_tree_attention_workspace, B, Hq, Hk, D, max_nodes, max_len)
