@@ -478,8 +478,10 @@ tcm_status tcm_qk_norm_rope_bwd_workspace(int64_t head_dim, int64_t* bytes);
  * dtype (q, out) TCM_F16 or TCM_BF16, the cache's dtype the same or TCM_E4M3.  Scores,
  * softmax and sums in fp32; the probabilities enter the second product as the
  * sum of two values of dtype (16 bits of them for TCM_BF16, 22 for TCM_F16, of
- * which those 2^-40 of a row's largest are the last).  D a multiple of 8 (16 for TCM_E4M3 caches), at most 256; Hq a multiple of
- * Hk; B and Hq at most 65535.
+ * which those 2^-40 of a row's largest are the last).  An infinite value of an attended key makes its element of the
+ * result that infinity (of both signs: NaN); where the key's probability is less than 2^-26 of the row's largest
+ * (2^-100 for TCM_BF16) it may be NaN instead.  D a multiple of 8 (16 for TCM_E4M3 caches), at most 256; Hq a multiple
+ * of Hk; B and Hq at most 65535.
  */
 tcm_status tcm_paged_attention(const tcm_heads* q, const tcm_cache* cache,
                                const int32_t* block_table, int64_t table_stride,
@@ -628,7 +630,8 @@ tcm_status tcm_gemm_w4(const void* X, int64_t ldx, const void* W, const void* sc
  *            are left as they were
  *   lse      NULL, or T x Hq fp32 (dense): log sum_j exp(scale * q . k_j)
  * block_table, lengths (the drafted tokens included), max_len, scale, window and the
- * cache as in tcm_paged_attention, and so are precision and the result of a row without keys.
+ * cache as in tcm_paged_attention, and so are precision, what infinite values give and the result of a row without
+ * keys.
  * With a tree tree_words * 64 >= max_nodes (TCM_ERR_INVALID_SHAPE), and tree 8-byte aligned.
  * T and max_nodes * Hq / Hk at most 2^30, B and Hq at most 65535.
  */

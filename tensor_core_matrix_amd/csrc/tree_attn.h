@@ -684,8 +684,9 @@ void tree_kernel(TreeArgs p) {
 #pragma unroll
                     for (int i = 0; i < RB; ++i) {
                         const float m2 = fmaxf(mx[i], top[i]);
-                        // (o may hold infinities: from the least factor on they stay)
-                        const float f = mx[i] == kNegInf ? 1.0f : fmaxf(__builtin_amdgcn_exp2f((mx[i] - m2) * scale), 0x1p-126f);
+                        // (Where it is 0, infinities in o become NaN.  Held at the least normal number it keeps them, but of
+                        // bf16's largest values too.)
+                        const float f = mx[i] == kNegInf ? 1.0f : __builtin_amdgcn_exp2f((mx[i] - m2) * scale);
                         mx[i] = m2;
                         sum[i] *= f;
 #pragma unroll
