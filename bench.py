@@ -29,8 +29,8 @@ Prints ONE JSON line.  `roofline` describes the dominant kernel: achieved =
 algorithmic flops per launch / median launch time, against the dense bf16
 MFMA peak.  `roofline.traffic` is the HBM bytes per launch measured with
 rocprofv3 counters (FETCH_SIZE + WRITE_SIZE, scaled by a copy kernel's
-reading) when profiles/traffic.json was taken on the current kernel sources,
-else null.  `cpu_baseline` is the fp64 oracle timed on the host on a bounded
+reading) when profiles/traffic.json was taken on the current sources of that
+kernel, else null.  `cpu_baseline` is the fp64 oracle timed on the host on a bounded
 sample of the same workload.
 """
 from __future__ import annotations
@@ -39,6 +39,7 @@ import argparse
 import hashlib
 import json
 import os
+import re
 import statistics
 import sys
 import threading
@@ -57,14 +58,30 @@ ORDER = ["bf16_8192", "mxfp8_8192", "mxfp6_8192", "mxfp4_8192", "nvfp4_8192", "b
 # input/output sets a workload rotates over (more than the 256 MB last-level
 # cache holds, so each call streams from HBM)
 SETS = {"batched": 3}
-def kernel_hash() -> str:
-    """Hash of every kernel and host source file of the library (csrc/)."""
-    h = hashlib.sha256()
-    csrc = os.path.join(ROOT, "tensor_core_matrix_amd", "csrc")
-    for f in sorted(os.listdir(csrc)):
-        if f.endswith((".h", ".hip", ".cpp")):
-            with open(os.path.join(csrc, f), "rb") as fh:
-                h.update(f.encode() + b"\0" + fh.read())
+CSRC = os.path.join(ROOT, "tensor_core_matrix_amd", "csrc")
+# the translation unit that holds each workload's kernel
+KERNEL_UNIT = {"bf16_8192": "gemm_tn.hip", "mxfp8_8192": "gemm_mx.hip", "mxfp6_8192": "gemm_mx6.hip",
+               "mxfp4_8192": "gemm_mx.hip", "nvfp4_8192": "gemm_nv4.hip", "bf16_8192_nn": "gemm_mn_b.hip",
+               "mxfp8_8192_mn": "gemm_mx_mn_ab.hip", "bf16_4096": "gemm_tn.hip", "batched": "gemm_tn.hip",
+               "tile_f16": "gemm_tn.hip"}
+
+
+def kernel_hash(workload: str, csrc: str = CSRC) -> str:
+    """Hash of what decides a workload's kernel: its translation unit, the products' dispatch, the
+    headers of csrc/ that these include, and the compiler's flags."""
+    from tensor_core_matrix_amd import build
+
+    todo, seen = [KERNEL_UNIT[workload], "tcm_api.cpp"], {}
+    while todo:
+        f = todo.pop()
+        path = os.path.join(csrc, f)
+        if f not in seen and os.path.exists(path):
+            with open(path, "rb") as fh:
+                seen[f] = fh.read()
+            todo += [m.decode() for m in re.findall(rb'^#include "([^"/]+)"', seen[f], re.M)]
+    h = hashlib.sha256(" ".join(f for f in build.DEVICE + build.COMMON if ROOT not in f).encode())
+    for f in sorted(seen):
+        h.update(b"\0" + f.encode() + b"\0" + seen[f])
     return h.hexdigest()[:16]
 
 
@@ -326,7 +343,7 @@ def load_traffic(workload: str):
     with open(path) as fh:
         t = json.load(fh)
     entry = t.get(workload)
-    if not entry or entry.get("kernel_hash") != kernel_hash():
+    if not entry or entry.get("kernel_hash") != kernel_hash(workload):
         return None
     return entry.get("bytes_per_launch")
 
