@@ -543,8 +543,9 @@ tcm_status tcm_cache_plan(int32_t* lengths, const int32_t* change, int32_t* bloc
  *   weight   NULL (ones), or D elements of weight_dtype: TCM_F32 or dtype
  *   sum      NULL, or T x D of dtype, rows lds apart: s rounded once
  *   Out      T x D of out_dtype (dtype or TCM_F32), rows ldo apart
- * Computed in fp32.  sum may be X or residual, and so may Out of the same type (the same
- * pointer and row stride); Out and sum overlap nothing else.  D a multiple of 8
+ * Computed in fp32, the squares too: a mean(s^2) past its range (|s| of 1.8e19 and more) is infinite and gives
+ * zeros, below 2^-126 it has fewer digits, and less than 2^-149 counts as 0.  sum may be X or residual, and so may
+ * Out of the same type (the same pointer and row stride); Out and sum overlap nothing else.  D a multiple of 8
  * (TCM_ERR_MISALIGNED), at most 32768; 16-byte aligned, row strides multiples of
  * 8 elements (16 bytes); a stride is not looked at where T <= 1.
  */
@@ -597,7 +598,8 @@ tcm_status tcm_add_rms_norm_bwd_workspace(int64_t T, int64_t D, int64_t* bytes);
  * of a group.  The result is rounded once.  With TCM_U4 the products with q and with zero may be
  * summed apart and subtracted (they are for TCM_BF16), so errors go by scale * (q + zero):
  * the result r satisfies |r - exact| <= u sum_k |x_k| scale (q + zero) (E2M1: |x_k w_k|),
- * u = (K / 32 + 96) 2^-24, plus the rounding.  A row of X with a value that
+ * u = (K / 32 + 96) 2^-24, plus the rounding, while a group's sum of |x_k| (q + zero) (E2M1: |x_k element|) is
+ * within fp32's normal numbers (which bf16 values of 1e36 and more may pass).  A row of X with a value that
  * is not finite has no finite result; rows do not reach each other's results.  The weights
  * are read once for each 64 rows, fastest where K is a multiple of 128 and scales and zeros
  * are 8-byte aligned.  K a multiple of 32, at most 2^20; ldx a multiple of 8 and at most 2^21;

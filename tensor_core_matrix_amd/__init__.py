@@ -36,7 +36,7 @@ A step that drafts several tokens at once (``step.py``, the same library):
     cache_plan(lengths, change, block_table, ...)          pages, slots and positions of new tokens
     add_rms_norm(x, weight, residual, ...)                 residual sum and norm
     add_rms_norm_mx_fp8(x, weight, residual, ...)          the same as MXFP8, for gemm_mx_fp8
-    add_rms_norm_bwd(dout, h, weight, ...)                 its gradients
+    add_rms_norm_bwd(dout, s, weight, ...)                 its gradients
     gemm_w4(x, w, scales, zeros, ...)                      few rows times 4-bit weights
     paged_tree_attention(q, k_cache, v_cache, ...)         a tree or chain of new tokens per sequence
 """

@@ -6,7 +6,7 @@
 //
 //   M   N      K     elements, group, type      us     weights and scales, TB/s
 //   1   4096   4096  U4, 128, zeros, bf16       8.3    1.1  (most of it the call itself)
-//   12  12288  4096  E2M1, 32, bf16             10.9   2.5
+//   12  12288  4096  E2M1, 32, bf16             10.5   2.6
 //   48  32003  4096  U4, 64, fp16 to fp32       28.5   2.4
 //
 // A wave takes 16 columns (rows of W) and blocks of 128 values of K: a lane reads 16 bytes, 32 values of one
@@ -393,8 +393,8 @@ bool share(W4Args& a, int rows, int cus) {
         return false;
     }
     // Waves side by side; the others share K.  As few as give no more workgroups than run at once: two on a compute
-    // unit, or one where X takes more than half of its LDS (12 rows, 12288 x 4096: 384 workgroups of 96 KB took 15.7 us
-    // in two rounds, 192 take 11.8).  A stage of X is a batch of each of the waves that share K, or all of K where it
+    // unit, or one where X takes more than half of its LDS (12 rows, 12288 x 4096: 384 workgroups of 96 KB take 14.5 us a
+    // call in two rounds, 192 in one 10.5; the kernels alone under a trace 15.4 and 11.6).  A stage of X is a batch of each of the waves that share K, or all of K where it
     // fits.
     constexpr int waves = waves_of(1), batch = 128 * depth_of(1);
     for (a.wn = 1;; a.wn *= 2) {

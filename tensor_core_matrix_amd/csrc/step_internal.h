@@ -74,7 +74,7 @@ struct W4Args {
 
 hipError_t launch_gemm_w4(const W4Args& a, int32_t dtype, bool e2m1, bool out_f32, int cus, hipStream_t st);
 
-// ---- attention of drafted tokens (tree_attn.hip) ------------------------------------
+// ---- attention of drafted tokens (tree_attn.h, tree_attn_{bf16,f16}.hip) ------------------------------------
 
 // A block of rows whose tiles lie in `parts` stretches, the first one that of the workgroup before (0: none).
 struct TreeSplit {
