@@ -28,8 +28,8 @@
 // joins those parts.  The host sees no length, so each workgroup adds up the tiles of the sequences itself.
 //
 // Measured on an MI355X, heads of 128, 32 over 8 (E4M3: 64 over 8), lengths drawn evenly up to the one given, bf16,
-// by the lengths drawn: 16 trees of 64 tokens, 4096 keys 69 to 77 us (of them 12 in the join), 32 trees of 16 over
-// an E4M3 cache of 4096 78 to 85, 5 tokens in a row on 2 x 65537 keys (fp16) 83 to 95, 4.6 TB/s, 9 on up to 700 16.
+// by the lengths drawn: 16 trees of 64 tokens, 4096 keys 66 to 77 us (of them 12 in the join), 32 trees of 16 over
+// an E4M3 cache of 4096 78 to 87, 5 tokens in a row on 2 x 65537 keys (fp16) 83 to 99, 9 on up to 700 16.
 // Long contexts with few rows are bound by memory; with 128 rows the matrix cores are busy for 42 % of the time,
 // vector instructions for 51 %, and the two waves of a SIMD wait for LDS, barriers and each other's products for the
 // rest: no single part left out (the second part of P, the exponentials, reads from LDS) gains more than 3 us.
