@@ -89,7 +89,8 @@ def _summed(x, residual, sum_out, shape, dev, out=None):
     """(x, residual, sum) as (address, stride) pairs, and the sum's tensor: x itself where nothing is added to it
     and out does not overwrite it."""
     dt = (x.dtype,)
-    if sum_out is None and (residual is not None or (out is not None and out.data_ptr() == x.data_ptr())):
+    onto = out is not None and x.numel() > 0 and out.data_ptr() == x.data_ptr()
+    if sum_out is None and (residual is not None or onto):
         sum_out = torch.empty(shape, dtype=x.dtype, device=x.device)
     none = (None, 0)
     return (_rows(x, "x", shape, dt, dev), none if residual is None else _rows(residual, "residual", shape, dt, dev),

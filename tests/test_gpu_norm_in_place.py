@@ -49,3 +49,8 @@ def test_a_sum_that_is_given_and_one_that_is_x():
     assert s is x  # nothing is copied where x stays
     y, s = tcm.add_rms_norm(x, out_dtype=F32)
     assert s is x
+
+
+def test_no_rows():
+    x = torch.empty((0, 64), dtype=BF, device=DEV)
+    assert tcm.add_rms_norm(x)[1] is x and tcm.add_rms_norm(x, out=x)[1] is x
